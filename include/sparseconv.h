@@ -389,6 +389,128 @@ sc_status sparseconv_dense_forward(const float* w_dense_dev, const float* input,
  * reads this handle (synchronise the stream first). */
 void sparseconv_destroy(sc_handle* h);
 
+/*
+ * ---- Sequence operators -----------------------------------------------------------------
+ *
+ * What stands between and beside pruned 1x1 layers applied to sequences (H = 1, W = L): a
+ * short causal convolution of each channel, a selective state space scan, and low-rank
+ * adapters added to a shared projection.  Each runs whole prompts and single positions.
+ *
+ * Conventions.
+ *  - A sequence tensor is (B, channels, L): its positions are contiguous, its batch and
+ *    channel strides are given in elements (>= 0; 0 repeats an input).  With L = 1 any channel
+ *    stride is a plain one, so a (B, channels) matrix of single positions is such a tensor.
+ *  - Activations (and conv states) have the type `dtype`; parameters, scan states and every
+ *    sum are fp32.  Results are rounded once, to nearest even, when they are stored.
+ *  - lengths (device, B entries, may be NULL): sequence b has positions 0 .. lengths[b]-1
+ *    (clamped to 0 .. L).  Past them outputs are 0, nothing is read into a result, and the
+ *    state stays what it was at the end.
+ *  - States.  initial_state (read; NULL: zeros) and final_state (written; NULL: not wanted)
+ *    hold num_slots states of one sequence each, `*_stride` elements apart.  Sequence b uses
+ *    slot slots[b] (device, B entries) or slot b where slots is NULL.  A sequence whose slot
+ *    is outside 0 .. num_slots-1 is idle: its outputs are 0 and no state is touched.  The two
+ *    may be the same buffer (states updated in place); otherwise they must not overlap.  Two
+ *    sequences of one call must not write the same slot.
+ *  - Outputs must not overlap inputs, except where it is said.
+ *  - Asynchronous on hip_stream (NULL: the default stream), no allocation, nothing
+ *    synchronised, capturable.  All checks happen before any launch.
+ * Errors: SC_EINVAL (NULL or misaligned pointer, unknown type or flag, overlap, workspace too
+ * small), SC_ESHAPE (a size or stride out of range), SC_EUNSUPPORTED (beyond a documented
+ * limit), SC_EDEVICE (launch failure).
+ */
+typedef enum { SC_F32 = 0, SC_BF16 = 1, SC_F16 = 2 } sc_dtype;
+
+#define SC_SEQ_SILU 1u     /* causal conv: out = v * sigmoid(v) of the sum v */
+#define SC_SEQ_SOFTPLUS 2u /* scan: step = log(1 + exp(dt + dt_bias)) instead of dt + dt_bias */
+
+typedef struct {
+  const void* x;             /* device, (B, D, L) */
+  void* out;                 /* device, (B, D, L) */
+  const float* weight;       /* device, D x K: weight[d*K + K-1] meets the present position */
+  const float* bias;         /* device, D entries; NULL: none */
+  const void* initial_state; /* per slot D x (K-1): the K-1 inputs before position 0, oldest first */
+  void* final_state;         /* per slot D x (K-1): the last K-1 inputs */
+  const int32_t* lengths;
+  const int32_t* slots;
+  int64_t x_batch, x_channel, out_batch, out_channel; /* strides */
+  int64_t initial_stride, final_stride;               /* between slots */
+  int32_t dtype, B, D, L, K, num_slots;               /* 1 <= K <= 8 */
+  uint32_t flags;                                     /* 0 or SC_SEQ_SILU */
+  int32_t reserved;                                   /* 0 */
+} sc_causal_conv;
+
+/*
+ * out[b,d,t] = act(bias[d] + sum_{k<K} weight[d,k] u[b,d,t-K+1+k]), u being the sequence with
+ * its initial state in front: the depthwise form of the convolution above, along one axis and
+ * causal.  B, L >= 0 (a call without sequences does nothing; L = 0 copies the states).
+ * Limits: B*D*ceil(L/8) < 2^31.
+ */
+sc_status sparseconv_causal_conv(const sc_causal_conv* a, void* hip_stream);
+
+typedef struct {
+  const void* x;              /* device, (B, D, L) */
+  const void* dt;             /* device, (B, D, L): the raw time steps */
+  const void* z;              /* device, (B, D, L): the gate; NULL: none */
+  const void* b;              /* device, (B, G, N, L) */
+  const void* c;              /* device, (B, G, N, L) */
+  void* out;                  /* device, (B, D, L) */
+  const float* A;             /* device, D x N */
+  const float* skip;          /* device, D entries ("D"); NULL: none */
+  const float* dt_bias;       /* device, D entries; NULL: none */
+  const float* initial_state; /* per slot D x N */
+  float* final_state;         /* per slot D x N */
+  const int32_t* lengths;
+  const int32_t* slots;
+  void* workspace;            /* device, 16-byte aligned, sparseconv_selective_scan_workspace bytes */
+  int64_t workspace_bytes;
+  int64_t x_batch, x_channel, dt_batch, dt_channel, z_batch, z_channel, out_batch, out_channel;
+  int64_t b_batch, b_group, b_state, c_batch, c_group, c_state; /* strides of b and c */
+  int64_t initial_stride, final_stride;                         /* between slots */
+  int32_t dtype, B, D, L, N, G, num_slots; /* 1 <= N <= 256; G divides D, channel d is of group d / (D/G) */
+  uint32_t flags;                          /* 0 or SC_SEQ_SOFTPLUS */
+} sc_selective_scan;
+
+/*
+ * The selective state space recurrence of each channel d over its N states, from h_{-1} = the
+ * initial state:
+ *     h_t[n] = exp(s_t A[d,n]) h_{t-1}[n] + s_t b_t[n] x_t,   s_t = dt_t + dt_bias[d] (softplus of it with
+ *     out_t  = (sum_n c_t[n] h_t[n] + skip[d] x_t) z_t sigmoid(z_t)                    SC_SEQ_SOFTPLUS)
+ * (without z, out_t is the first factor).  b, c: strides in elements, positions contiguous; with
+ * L = 1 the states' stride may be any.  B, L >= 0.  Limits: B*D < 2^31, L < 2^30.
+ */
+sc_status sparseconv_selective_scan(const sc_selective_scan* a, void* hip_stream);
+
+/* Device workspace a scan with these sizes needs, in bytes (0 if none).  Only the sizes of *a
+ * are looked at.  Errors: SC_EINVAL (NULL), SC_ESHAPE, SC_EUNSUPPORTED. */
+sc_status sparseconv_selective_scan_workspace(const sc_selective_scan* a, int64_t* bytes);
+
+typedef struct {
+  const void* x;        /* device, (B, C, L) */
+  const void* base;     /* device, (B, M, L): the shared projection's output; NULL: zeros */
+  void* out;            /* device, (B, M, L); may be base itself (same pointer and strides) */
+  const void* down;     /* device, adapters x R x C, of type dtype, 16-byte aligned */
+  const void* up;       /* device, adapters x M x R, of type dtype, 16-byte aligned */
+  const float* scale;   /* device, one per adapter; NULL: 1 */
+  const int32_t* index; /* device, B entries: the adapter of each sequence; outside
+                           0 .. adapters-1: none (out = base) */
+  void* workspace;      /* device, 16-byte aligned, sparseconv_adapter_workspace bytes */
+  int64_t workspace_bytes;
+  int64_t x_batch, x_channel, base_batch, base_channel, out_batch, out_channel;
+  int32_t dtype, B, C, M, L, R, adapters; /* 1 <= R <= 128 */
+  int32_t reserved;                       /* 0 */
+} sc_adapter;
+
+/*
+ * out[b] = base[b] + scale[r] * up[r] (down[r] x[b]) with r = index[b]: the low-rank adapters of
+ * many requests in one call, beside a projection that they share (a packed 1x1 layer).
+ * B, L >= 0, M, C, adapters >= 1.  Limits: B*C*R, B*M*R < 2^31, L < 2^30.
+ */
+sc_status sparseconv_adapter_apply(const sc_adapter* a, void* hip_stream);
+
+/* Device workspace such a call needs, in bytes (0 if none).  Only the sizes and strides of *a are
+ * looked at.  Errors as sparseconv_selective_scan_workspace. */
+sc_status sparseconv_adapter_workspace(const sc_adapter* a, int64_t* bytes);
+
 /* Message of the calling thread's last failure ("" if none).  Valid until that thread's
  * next call into the library. */
 const char* sparseconv_last_error(void);

@@ -9,7 +9,7 @@ The functions keep the C names:
     sparseconv_pack, sparseconv_forward, sparseconv_forward_workspace,
     sparseconv_workspace_size, sparseconv_query, sparseconv_export_packed,
     sparseconv_export_words, sparseconv_destroy, sparseconv_last_error
-plus ``Handle`` (owns a packed filter bank and destroys it when collected).  The dense
+plus the sequence operators (sequence.py) and ``Handle`` (owns a packed filter bank and destroys it when collected).  The dense
 direct baseline is a Handle packed with SC_PACK_ALL_TAPS (every filter tap stored).
 """
 from __future__ import annotations
@@ -48,7 +48,8 @@ EXPORTED = ("sparseconv_pack", "sparseconv_forward", "sparseconv_forward_workspa
             "sparseconv_query", "sparseconv_export_packed", "sparseconv_export_words",
             "sparseconv_export_kernel_source", "sparseconv_launch_info", "sparseconv_device_status",
             "sparseconv_dense_forward", "sparseconv_forward_noalloc", "sparseconv_tune", "sparseconv_destroy",
-            "sparseconv_last_error")
+            "sparseconv_causal_conv", "sparseconv_selective_scan", "sparseconv_selective_scan_workspace",
+            "sparseconv_adapter_apply", "sparseconv_adapter_workspace", "sparseconv_last_error")
 
 
 class sc_weights(ctypes.Structure):
@@ -398,3 +399,8 @@ class Handle:
             self.close()
         except Exception:
             pass
+
+
+from .sequence import (adapter_apply, causal_conv, causal_conv_step, selective_scan, selective_scan_step,  # noqa: E402,F401
+                       selective_scan_workspace, sparseconv_adapter_apply, sparseconv_adapter_workspace,
+                       sparseconv_causal_conv, sparseconv_selective_scan, sparseconv_selective_scan_workspace)

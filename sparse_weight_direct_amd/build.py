@@ -9,7 +9,8 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libsparseconv.so")
 PROBE_LIB = os.path.join(HERE, "libscprobe.so")  # roof probes timed by the benchmark
 PROBE_SOURCE = os.path.join(HERE, "csrc", "probes.hip")
-SOURCES = [os.path.join(HERE, "csrc", f) for f in ("kernels.hip", "escoin.hip", "dense.hip", "pack.cpp", "bake.cpp", "api.cpp")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("kernels.hip", "escoin.hip", "dense.hip", "pack.cpp", "bake.cpp", "api.cpp",
+                                               "causal_conv.hip", "selective_scan.hip", "adapter.hip", "sequence.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # Packed FP32 instructions are disabled for all device code: hipcc would otherwise form

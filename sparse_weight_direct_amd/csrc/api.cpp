@@ -64,6 +64,13 @@ bool fail_alloc_hook() {
 
 }  // namespace
 
+namespace sc {
+
+// The calling thread's error message, for the entry points in sequence.cpp.
+int report(int status, const std::string& msg) { return fail((sc_status)status, msg); }
+
+}  // namespace sc
+
 // One launch plan of a handle with its own kernel stream and tables on the device.  A handle
 // holds the default plan (variant 0, the most positions per lane that fit) and a few plans
 // with fewer positions per lane or fewer rows per wavefront, which make more work units: the

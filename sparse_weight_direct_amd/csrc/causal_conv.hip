@@ -1,0 +1,125 @@
+// Short causal convolution of each channel (sparseconv_causal_conv).
+//
+//   out[b,d,t] = act(bias[d] + sum_k w[d,k] u[b,d,t-K+1+k]),  u = the initial state, then x.
+#include <hip/hip_runtime.h>
+
+#include "sequence_device.h"
+
+namespace sc {
+
+namespace {
+
+constexpr int kV = 8;  // positions per thread: at least K - 1, so only a row's first thread meets the state
+
+template <class T, int K, bool SILU>
+__global__ __launch_bounds__(256) void causal_conv_rows(const sc_causal_conv a) {
+  typedef typename Pack<T, kV>::type Vec;
+  const int nv = max(1, (a.L + kV - 1) / kV);
+  const uint32_t id = blockIdx.x * 256u + threadIdx.x;
+  if (id >= (uint32_t)a.B * a.D * nv) return;
+  const int row = id / nv, t0 = (id - row * nv) * kV;
+  const int b = row / a.D, d = row - b * a.D;
+  const int slot = slot_of(a.slots, a.num_slots, b);
+  const int len = slot < 0 ? 0 : length_of(a.lengths, a.L, b);
+  const T* x = static_cast<const T*>(a.x) + b * a.x_batch + d * a.x_channel;
+  T* out = static_cast<T*>(a.out) + b * a.out_batch + d * a.out_channel;
+  float w[K];
+#pragma unroll
+  for (int k = 0; k < K; k++) w[k] = a.weight[(int64_t)d * K + k];
+  const float bias = a.bias ? a.bias[d] : 0.0f;
+
+  T u[K - 1 + kV];  // positions t0-K+1 .. t0+kV-1
+  const bool whole = t0 + kV <= a.L;
+  if (whole) {
+    const Vec v = *reinterpret_cast<const Vec*>(x + t0);
+#pragma unroll
+    for (int i = 0; i < kV; i++) u[K - 1 + i] = v[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < kV; i++) u[K - 1 + i] = t0 + i < a.L ? x[t0 + i] : T(0);
+  }
+  if (t0 > 0) {
+    const Vec v = *reinterpret_cast<const Vec*>(x + t0 - kV);
+#pragma unroll
+    for (int j = 0; j < K - 1; j++) u[j] = v[kV - K + 1 + j];
+  } else {
+    const T* first = static_cast<const T*>(a.initial_state);
+    if (first && slot >= 0) {
+      first += slot * a.initial_stride + (int64_t)d * (K - 1);
+#pragma unroll
+      for (int j = 0; j < K - 1; j++) u[j] = first[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < K - 1; j++) u[j] = T(0);
+    }
+    // The state is read (above) and written by this thread alone, so it may be updated in place.
+    if (K > 1 && a.final_state && slot >= 0) {
+      T* last = static_cast<T*>(a.final_state) + slot * a.final_stride + (int64_t)d * (K - 1);
+#pragma unroll
+      for (int j = 0; j < K - 1; j++) {
+        const int t = len - (K - 1) + j;
+        T v = t >= 0 ? x[t] : T(0);
+#pragma unroll
+        for (int i = 0; i < K - 1; i++)
+          if (t == i - (K - 1)) v = u[i];
+        last[j] = v;
+      }
+    }
+  }
+  T y[kV];
+#pragma unroll
+  for (int i = 0; i < kV; i++) {
+    float v = bias;
+#pragma unroll
+    for (int k = 0; k < K; k++) v = fmaf(w[k], (float)u[i + k], v);
+    if (SILU) v = silu(v);
+    y[i] = T(t0 + i < len ? v : 0.0f);
+  }
+  if (whole) {
+    Vec v;
+#pragma unroll
+    for (int i = 0; i < kV; i++) v[i] = y[i];
+    *reinterpret_cast<Vec*>(out + t0) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kV; i++)
+      if (t0 + i < a.L) out[t0 + i] = y[i];
+  }
+}
+
+template <class T, int K, bool SILU>
+int launch_one(const sc_causal_conv& a, hipStream_t st) {
+  const int64_t n = (int64_t)a.B * a.D * std::max(1, (a.L + kV - 1) / kV);
+  hipLaunchKernelGGL((causal_conv_rows<T, K, SILU>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, a);
+  return (int)hipGetLastError();
+}
+
+template <class T, int K>
+int launch_act(const sc_causal_conv& a, hipStream_t st) {
+  return a.flags & SC_SEQ_SILU ? launch_one<T, K, true>(a, st) : launch_one<T, K, false>(a, st);
+}
+
+template <class T>
+int launch_taps(const sc_causal_conv& a, hipStream_t st) {
+  switch (a.K) {
+    case 1: return launch_act<T, 1>(a, st);
+    case 2: return launch_act<T, 2>(a, st);
+    case 3: return launch_act<T, 3>(a, st);
+    case 4: return launch_act<T, 4>(a, st);
+    case 5: return launch_act<T, 5>(a, st);
+    case 6: return launch_act<T, 6>(a, st);
+    case 7: return launch_act<T, 7>(a, st);
+    default: return launch_act<T, 8>(a, st);
+  }
+}
+
+}  // namespace
+
+int launch_causal_conv(const sc_causal_conv& a, void* stream) {
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (a.dtype == SC_F32) return launch_taps<float>(a, st);
+  if (a.dtype == SC_BF16) return launch_taps<__bf16>(a, st);
+  return launch_taps<_Float16>(a, st);
+}
+
+}  // namespace sc
