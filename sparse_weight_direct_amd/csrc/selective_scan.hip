@@ -3,77 +3,388 @@
 //   h_t[n] = exp(s_t A[d,n]) h_{t-1}[n] + s_t b_t[n] x_t,   out_t = (sum_n c_t[n] h_t[n] + skip[d] x_t) silu(z_t)
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "sequence_device.h"
+#include "xcd.h"
 
 namespace sc {
 
 namespace {
 
-// One wavefront per (sequence, channel), its lanes over the states, one position after another.
-template <class T>
-__global__ __launch_bounds__(256) void scan_rows(const sc_selective_scan a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= (int64_t)a.B * a.D) return;
-  const int b = row / a.D, d = row - (int64_t)b * a.D, g = d / (a.D / a.G);
+// ---- Prompts
+//
+// The steps h -> a h + v of one state compose: two segments (P1, S1), (P2, S2), each its product
+// of a's and its end state from 0, make (P1 P2, P2 S1 + S2).  Sixteen lanes hold TI consecutive
+// positions each of one channel; a lane walks its positions once for (P, S), the sixteen are
+// scanned by row shifts (DPP, 4 steps), and the lane walks again from the state it now knows,
+// adding c h to its outputs, which stay in registers over all states n.  P needs no product over
+// the positions: it is exp(A sum s).
+//
+// A workgroup takes 16 channels of one group (4 a wavefront) and all its positions, 16 TI at a
+// time, so one copy of b and c in LDS (fp32, kStates states at a time) serves 16 channels.
+// Per (position, channel, state): 1 exp2, 2 products and 3 FMAs, and the scan's 20 instructions
+// shared by TI positions.
+
+constexpr int kRows = 16;     // channels per workgroup
+constexpr int kStates = 16;   // states of b and c in LDS at a time
+
+// Pitch of a channel's {A, h} in LDS: one past N, so that the four channels of a wavefront read other
+// banks; at N = 256 none, which keeps the workgroup at 64 KB.
+__host__ __device__ constexpr int ah_pitch(int N) { return N < 256 ? N + 1 : 256; }
+
+enum Part { kWhole, kEnds, kSegment };
+
+struct Split {
+  int chunks;     // 16 TI positions each, per segment
+  int segments;
+  float* state;   // [B][segments][D][N]: entry 0 the initial state, entry s the end of segment s-1 from 0
+  float* sum;     // [B][segments][D]: entry s the sum of segment s-1's steps
+};
+
+template <int SHIFT>
+__device__ __forceinline__ float row_shr(float old, float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, old), __builtin_bit_cast(int, v),
+                                                               0x110 + SHIFT, 0xf, 0xf, false));
+}
+
+template <int SHIFT>
+__device__ __forceinline__ void compose(float& P, float& S) {
+  const float p = row_shr<SHIFT>(1.0f, P), s = row_shr<SHIFT>(0.0f, S);
+  S = fmaf(P, s, S);
+  P *= p;
+}
+
+// TI values of a row from position t0 on; those at or past `end` are 0 and not read.
+template <class T, int TI>
+__device__ __forceinline__ void load_row(const T* p, int t0, int end, float (&v)[TI]) {
+  constexpr int V = TI * sizeof(T) >= 16 ? 16 / sizeof(T) : TI;
+  typedef typename Pack<T, V>::type Vec;
+  if (t0 + TI <= end) {
+#pragma unroll
+    for (int i = 0; i < TI; i += V) {
+      const Vec w = *reinterpret_cast<const Vec*>(p + t0 + i);
+#pragma unroll
+      for (int j = 0; j < V; j++) v[i + j] = (float)w[j];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < TI; i++) v[i] = t0 + i < end ? (float)p[t0 + i] : 0.0f;
+  }
+}
+
+template <class T, int TI>
+__device__ __forceinline__ void store_row(T* p, int t0, int end, const float (&v)[TI]) {
+  constexpr int V = TI * sizeof(T) >= 16 ? 16 / sizeof(T) : TI;
+  typedef typename Pack<T, V>::type Vec;
+  if (t0 + TI <= end) {
+#pragma unroll
+    for (int i = 0; i < TI; i += V) {
+      Vec w;
+#pragma unroll
+      for (int j = 0; j < V; j++) w[j] = T(v[i + j]);
+      *reinterpret_cast<Vec*>(p + t0 + i) = w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < TI; i++)
+      if (t0 + i < end) p[t0 + i] = T(v[i]);
+  }
+}
+
+template <class T, int TI, Part PART>
+__global__ __launch_bounds__(256) void scan_prompt(const sc_selective_scan a, const Split sp) {
+  constexpr int CH = 16 * TI;                    // positions per chunk
+  constexpr int MATS = PART == kEnds ? 1 : 2;    // b, and c where outputs are wanted
+  extern __shared__ float lds[];
+  float4* bc = reinterpret_cast<float4*>(lds);                              // [MATS][kStates][TI/4][16] quads of positions
+  float2* ah = reinterpret_cast<float2*>(lds + MATS * kStates * CH);        // [kRows][ah_pitch(N)]: {A log2(e), h}
+  const int tid = threadIdx.x, lane = tid & 15, row = tid >> 4;
+  const int share = a.D / a.G, tiles = (share + kRows - 1) / kRows;
+  const int segments = PART == kWhole ? 1 : PART == kEnds ? sp.segments - 1 : sp.segments;
+  int id = xcd_logical(blockIdx.x, gridDim.x);
+  const int tile = id % tiles;
+  id /= tiles;
+  const int seg = id % segments;
+  id /= segments;
+  const int g = id % a.G, b = id / a.G;
+  const int in_group = tile * kRows + row;
+  const bool live = in_group < share;
+  const int d = g * share + min(in_group, share - 1);
   const int slot = slot_of(a.slots, a.num_slots, b);
   const int len = slot < 0 ? 0 : length_of(a.lengths, a.L, b);
+  const int N = a.N, AH = ah_pitch(N);
   const T* x = static_cast<const T*>(a.x) + b * a.x_batch + d * a.x_channel;
   const T* dt = static_cast<const T*>(a.dt) + b * a.dt_batch + d * a.dt_channel;
   const T* z = a.z ? static_cast<const T*>(a.z) + b * a.z_batch + d * a.z_channel : nullptr;
-  const T* bm = static_cast<const T*>(a.b) + b * a.b_batch + g * a.b_group;
-  const T* cm = static_cast<const T*>(a.c) + b * a.c_batch + g * a.c_group;
   T* out = static_cast<T*>(a.out) + b * a.out_batch + d * a.out_channel;
   const float skip = a.skip ? a.skip[d] : 0.0f, bias = a.dt_bias ? a.dt_bias[d] : 0.0f;
-  float A[4], h[4];
-#pragma unroll
-  for (int j = 0; j < 4; j++) {
-    const int n = lane + 64 * j;
-    A[j] = n < a.N ? a.A[(int64_t)d * a.N + n] * kLog2e : 0.0f;
-    h[j] = n < a.N && a.initial_state && slot >= 0 ? a.initial_state[slot * a.initial_stride + (int64_t)d * a.N + n] : 0.0f;
+  const bool soft = a.flags & SC_SEQ_SOFTPLUS;
+
+  // the starting states: sixteen lanes over the states of their channel
+  for (int n = lane; n < N; n += 16) {
+    const float A = a.A[(int64_t)d * N + n] * kLog2e;
+    float h = 0.0f;
+    if (PART == kSegment) {
+      const float* st = sp.state + (((int64_t)b * sp.segments) * a.D + d) * N + n;
+      const float* sm = sp.sum + (int64_t)b * sp.segments * a.D + d;
+      h = st[0];
+      for (int s = 1; s <= seg; s++) h = fmaf(exp2_fast(A * sm[(int64_t)s * a.D]), h, st[(int64_t)s * a.D * N]);
+    } else if (a.initial_state && slot >= 0 && (PART == kWhole || seg == 0)) {
+      h = a.initial_state[slot * a.initial_stride + (int64_t)d * N + n];
+    }
+    if (PART == kEnds) {
+      if (seg == 0 && live) sp.state[(((int64_t)b * sp.segments) * a.D + d) * N + n] = h;
+      h = 0.0f;
+    }
+    ah[row * AH + n] = make_float2(A, h);
   }
-  for (int t = 0; t < len; t++) {
-    const float xt = (float)x[t], raw = (float)dt[t] + bias;
-    const float s = a.flags & SC_SEQ_SOFTPLUS ? softplus(raw) : raw;
-    float y = 0.0f;
+
+  const int first = PART == kWhole ? 0 : seg * sp.chunks * CH;
+  const int last = PART == kWhole ? a.L : min(a.L, first + sp.chunks * CH);
+  float total = 0.0f;
+  for (int c0 = first; c0 < last; c0 += CH) {
+    const int t0 = c0 + lane * TI;
+    float s[TI], sx[TI], y[TI], sum = 0.0f;
+    if (c0 >= len) {  // nothing of the sequence is left (the same for the whole workgroup)
+      if (PART == kEnds) break;
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const int n = lane + 64 * j;
-      if (n < a.N) {
-        h[j] = fmaf(exp2_fast(s * A[j]), h[j], s * xt * (float)bm[n * a.b_state + t]);
-        y = fmaf((float)cm[n * a.c_state + t], h[j], y);
+      for (int i = 0; i < TI; i++) y[i] = 0.0f;
+      if (live) store_row<T, TI>(out, t0, a.L, y);
+      continue;
+    }
+    load_row<T, TI>(x, t0, len, y);
+    load_row<T, TI>(dt, t0, len, s);
+#pragma unroll
+    for (int i = 0; i < TI; i++) {
+      const float raw = s[i] + bias;
+      s[i] = t0 + i < len ? (soft ? softplus(raw) : raw) : 0.0f;
+      sx[i] = s[i] * y[i];
+      y[i] *= skip;
+      sum += s[i];
+    }
+    total += sum;
+    for (int n0 = 0; n0 < N; n0 += kStates) {
+      const int ns = min(kStates, N - n0);
+      __syncthreads();
+      // b and c of these states: 8 positions a thread, 0 past the length
+      for (int i = tid; i < MATS * ns * (CH / 8); i += 256) {
+        const int q = i % (CH / 8), m = i / (CH / 8), n = m % ns, mat = m / ns;
+        const T* p = mat ? static_cast<const T*>(a.c) + b * a.c_batch + g * a.c_group + (n0 + n) * a.c_state
+                         : static_cast<const T*>(a.b) + b * a.b_batch + g * a.b_group + (n0 + n) * a.b_state;
+        float v[8];
+        load_row<T, 8>(p, c0 + q * 8, len, v);
+        float4* to = bc + (mat * kStates + n) * (CH / 4);
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+          const int k = q * 2 + j;  // quad of the chunk: lane k / (TI/4)
+          to[(k % (TI / 4)) * 16 + k / (TI / 4)] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        }
+      }
+      __syncthreads();
+      for (int n = 0; n < ns; n++) {
+        const float2 Ah = ah[row * AH + n0 + n];
+        float av[TI], bv[TI];
+        float P = exp2_fast(Ah.x * sum), S = 0.0f;
+#pragma unroll
+        for (int k = 0; k < TI / 4; k++) {
+          const float4 q = bc[n * (CH / 4) + k * 16 + lane];
+          const float w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            const int i = 4 * k + j;
+            av[i] = exp2_fast(s[i] * Ah.x);
+            bv[i] = sx[i] * w[j];
+            S = fmaf(av[i], S, bv[i]);
+          }
+        }
+        compose<1>(P, S);
+        compose<2>(P, S);
+        compose<4>(P, S);
+        compose<8>(P, S);
+        if (PART != kEnds) {
+          float h = fmaf(row_shr<1>(1.0f, P), Ah.y, row_shr<1>(0.0f, S));
+#pragma unroll
+          for (int k = 0; k < TI / 4; k++) {
+            const float4 q = bc[(kStates + n) * (CH / 4) + k * 16 + lane];
+            const float w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+              const int i = 4 * k + j;
+              h = fmaf(av[i], h, bv[i]);
+              y[i] = fmaf(w[j], h, y[i]);
+            }
+          }
+        }
+        if (lane == 15) ah[row * AH + n0 + n].y = fmaf(P, Ah.y, S);
       }
     }
-    for (int m = 32; m; m >>= 1) y += __shfl_xor(y, m);
-    y = fmaf(skip, xt, y);
-    if (z) y *= silu((float)z[t]);
-    if (lane == 0) out[t] = T(y);
-  }
-  for (int t = len + lane; t < a.L; t += 64) out[t] = T(0.0f);
-  if (a.final_state && slot >= 0)
+    if (PART != kEnds && live) {
+      if (z) {
+        float g8[TI];
+        load_row<T, TI>(z, t0, len, g8);
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const int n = lane + 64 * j;
-      if (n < a.N) a.final_state[slot * a.final_stride + (int64_t)d * a.N + n] = h[j];
+        for (int i = 0; i < TI; i++) y[i] *= silu(g8[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < TI; i++) y[i] = t0 + i < len ? y[i] : 0.0f;
+      store_row<T, TI>(out, t0, a.L, y);
     }
+  }
+  __syncthreads();
+  if (!live) return;
+  if (PART == kEnds) {
+    float* st = sp.state + (((int64_t)b * sp.segments + seg + 1) * a.D + d) * N;
+    for (int n = lane; n < N; n += 16) st[n] = ah[row * AH + n].y;
+#pragma unroll
+    for (int m = 8; m; m >>= 1) total += __shfl_xor(total, m);
+    if (lane == 0) sp.sum[((int64_t)b * sp.segments + seg + 1) * a.D + d] = total;
+  } else if (a.final_state && slot >= 0 && seg == segments - 1) {
+    for (int n = lane; n < N; n += 16) a.final_state[slot * a.final_stride + (int64_t)d * N + n] = ah[row * AH + n].y;
+  }
+}
+
+// ---- Single positions
+//
+// The states are all that counts: 8 N bytes a channel, read and written once.  Q lanes share a
+// channel, four states a lane and pass (one 16-byte load), and sum its output by row shifts.
+template <class T, int Q>
+__global__ __launch_bounds__(256) void scan_token(const sc_selective_scan a) {
+  typedef typename Pack<float, 4>::type F4;
+  const int64_t id = (int64_t)blockIdx.x * (256 / Q) + threadIdx.x / Q;
+  const int lane = threadIdx.x % Q;
+  const bool live = id < (int64_t)a.B * a.D;
+  const int64_t at = live ? id : (int64_t)a.B * a.D - 1;
+  const int b = at / a.D, d = at - (int64_t)b * a.D, g = d / (a.D / a.G);
+  const int slot = slot_of(a.slots, a.num_slots, b);
+  const bool on = live && slot >= 0 && length_of(a.lengths, 1, b) == 1;
+  T* out = static_cast<T*>(a.out) + b * a.out_batch + d * a.out_channel;
+  const float x = (float)static_cast<const T*>(a.x)[b * a.x_batch + d * a.x_channel];
+  const float raw = (float)static_cast<const T*>(a.dt)[b * a.dt_batch + d * a.dt_channel] + (a.dt_bias ? a.dt_bias[d] : 0.0f);
+  const float s = a.flags & SC_SEQ_SOFTPLUS ? softplus(raw) : raw;
+  const float sx = s * x;
+  const T* bm = static_cast<const T*>(a.b) + b * a.b_batch + g * a.b_group;
+  const T* cm = static_cast<const T*>(a.c) + b * a.c_batch + g * a.c_group;
+  const float* from = a.initial_state && slot >= 0 ? a.initial_state + slot * a.initial_stride + (int64_t)d * a.N : nullptr;
+  float* to = a.final_state && slot >= 0 && live ? a.final_state + slot * a.final_stride + (int64_t)d * a.N : nullptr;
+  const float* A = a.A + (int64_t)d * a.N;
+  float y = 0.0f;
+  for (int n0 = lane * 4; n0 < a.N; n0 += 4 * Q) {
+    const int ns = min(4, a.N - n0);
+    F4 h = {0.0f, 0.0f, 0.0f, 0.0f}, w = h;
+    if (ns == 4) {
+      w = *reinterpret_cast<const F4*>(A + n0);
+      if (from) h = *reinterpret_cast<const F4*>(from + n0);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 3; j++)
+        if (j < ns) {
+          w[j] = A[n0 + j];
+          if (from) h[j] = from[n0 + j];
+        }
+    }
+    if (on) {
+#pragma unroll
+      for (int j = 0; j < 4; j++)
+        if (j < ns) {
+          h[j] = fmaf(exp2_fast(s * (w[j] * kLog2e)), h[j], sx * (float)bm[(n0 + j) * a.b_state]);
+          y = fmaf((float)cm[(n0 + j) * a.c_state], h[j], y);
+        }
+    }
+    if (to) {
+      if (ns == 4)
+        *reinterpret_cast<F4*>(to + n0) = h;
+      else
+#pragma unroll
+        for (int j = 0; j < 3; j++)
+          if (j < ns) to[n0 + j] = h[j];
+    }
+  }
+#pragma unroll
+  for (int m = Q / 2; m; m >>= 1) y += __shfl_xor(y, m);
+  if (lane == 0 && live) {
+    y = fmaf(a.skip ? a.skip[d] : 0.0f, x, y);
+    if (a.z) y *= silu((float)static_cast<const T*>(a.z)[b * a.z_batch + d * a.z_channel]);
+    *out = T(on ? y : 0.0f);
+  }
+}
+
+template <class T, int Q>
+int launch_token(const sc_selective_scan& a, hipStream_t st) {
+  const int64_t rows = (int64_t)a.B * a.D, per = 256 / Q;
+  hipLaunchKernelGGL((scan_token<T, Q>), dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, st, a);
+  return (int)hipGetLastError();
+}
+
+// How a prompt's scan is cut: positions per lane, and segments of the axis where there are few rows.
+struct Plan {
+  int ti, chunks, segments;
+  int64_t groups;  // workgroups of a segment
+};
+
+Plan plan_of(const sc_selective_scan& a, int cus) {
+  Plan p;
+  p.ti = a.L <= 64 ? 4 : a.L <= 128 ? 8 : 16;
+  const int64_t share = a.D / a.G;
+  p.groups = (int64_t)a.B * a.G * ((share + kRows - 1) / kRows);
+  const int chunks = std::max(1, (a.L + 16 * p.ti - 1) / (16 * p.ti));
+  int64_t want = 1;
+  if (p.groups < 2 * cus) want = (4 * cus + p.groups - 1) / p.groups;
+  const int most = std::max(1, std::min(chunks / 2, 64));
+  int segments = (int)std::min<int64_t>(want, most);
+  p.chunks = (chunks + segments - 1) / segments;
+  p.segments = (chunks + p.chunks - 1) / p.chunks;
+  return p;
+}
+
+template <class T, int TI, Part PART>
+int launch_part(const sc_selective_scan& a, const Plan& p, const Split& sp, hipStream_t st) {
+  const int lds = ((PART == kEnds ? 1 : 2) * kStates * 16 * TI + kRows * ah_pitch(a.N) * 2) * 4;
+  const int64_t blocks = p.groups * (PART == kWhole ? 1 : PART == kEnds ? p.segments - 1 : p.segments);
+  hipLaunchKernelGGL((scan_prompt<T, TI, PART>), dim3((unsigned)blocks), dim3(256), lds, st, a, sp);
+  return (int)hipGetLastError();
+}
+
+template <class T, int TI>
+int launch_prompt(const sc_selective_scan& a, const Plan& p, hipStream_t st) {
+  Split sp{};
+  if (p.segments == 1) return launch_part<T, TI, kWhole>(a, p, sp, st);
+  sp.chunks = p.chunks;
+  sp.segments = p.segments;
+  sp.state = static_cast<float*>(a.workspace);
+  sp.sum = sp.state + (int64_t)a.B * p.segments * a.D * a.N;
+  if (const int e = launch_part<T, TI, kEnds>(a, p, sp, st)) return e;
+  return launch_part<T, TI, kSegment>(a, p, sp, st);
 }
 
 template <class T>
-int launch_type(const sc_selective_scan& a, hipStream_t st) {
-  const int64_t rows = (int64_t)a.B * a.D;
-  hipLaunchKernelGGL((scan_rows<T>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, a);
-  return (int)hipGetLastError();
+int launch_type(const sc_selective_scan& a, int cus, hipStream_t st) {
+  if (a.L == 1) {
+    if (a.N <= 4) return launch_token<T, 1>(a, st);
+    if (a.N <= 8) return launch_token<T, 2>(a, st);
+    if (a.N <= 16) return launch_token<T, 4>(a, st);
+    if (a.N <= 32) return launch_token<T, 8>(a, st);
+    return launch_token<T, 16>(a, st);
+  }
+  const Plan p = plan_of(a, cus);
+  if (p.ti == 4) return launch_prompt<T, 4>(a, p, st);
+  if (p.ti == 8) return launch_prompt<T, 8>(a, p, st);
+  return launch_prompt<T, 16>(a, p, st);
 }
 
 }  // namespace
 
-int64_t scan_workspace(const sc_selective_scan&, int) { return 0; }
+int64_t scan_workspace(const sc_selective_scan& a, int cus) {
+  if (a.L <= 1) return 0;
+  const Plan p = plan_of(a, cus);
+  return p.segments == 1 ? 0 : (int64_t)a.B * p.segments * a.D * (a.N + 1) * 4;
+}
 
-int launch_selective_scan(const sc_selective_scan& a, int, void* stream) {
+int launch_selective_scan(const sc_selective_scan& a, int cus, void* stream) {
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  if (a.dtype == SC_F32) return launch_type<float>(a, st);
-  if (a.dtype == SC_BF16) return launch_type<__bf16>(a, st);
-  return launch_type<_Float16>(a, st);
+  if (a.dtype == SC_F32) return launch_type<float>(a, cus, st);
+  if (a.dtype == SC_BF16) return launch_type<__bf16>(a, cus, st);
+  return launch_type<_Float16>(a, cus, st);
 }
 
 }  // namespace sc
