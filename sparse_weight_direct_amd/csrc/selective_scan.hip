@@ -48,11 +48,24 @@ __device__ __forceinline__ float row_shr(float old, float v) {
                                                                0x110 + SHIFT, 0xf, 0xf, false));
 }
 
-template <int SHIFT>
-__device__ __forceinline__ void compose(float& P, float& S) {
-  const float p = row_shr<SHIFT>(1.0f, P), s = row_shr<SHIFT>(0.0f, S);
-  S = fmaf(P, s, S);
-  P *= p;
+// Inclusive scan of (P, S) over the sixteen lanes of a DPP row.  A lane without a source 1, 2, 4 or 8
+// lanes below keeps its values (its write is disabled), which is the identity step, so the shifts
+// need no constants: 8 instructions and the wait states between a write and its DPP read.
+__device__ __forceinline__ void compose16(float& P, float& S) {
+  asm("s_nop 1\n\t"
+      "v_fmac_f32_dpp %1, %1, %0 row_shr:1 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32_dpp %0, %0, %0 row_shr:1 row_mask:0xf bank_mask:0xf\n\t"
+      "s_nop 1\n\t"
+      "v_fmac_f32_dpp %1, %1, %0 row_shr:2 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32_dpp %0, %0, %0 row_shr:2 row_mask:0xf bank_mask:0xf\n\t"
+      "s_nop 1\n\t"
+      "v_fmac_f32_dpp %1, %1, %0 row_shr:4 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32_dpp %0, %0, %0 row_shr:4 row_mask:0xf bank_mask:0xf\n\t"
+      "s_nop 1\n\t"
+      "v_fmac_f32_dpp %1, %1, %0 row_shr:8 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32_dpp %0, %0, %0 row_shr:8 row_mask:0xf bank_mask:0xf\n\t"
+      "s_nop 1"
+      : "+v"(P), "+v"(S));
 }
 
 // TI values of a row from position t0 on; those at or past `end` are 0 and not read.
@@ -93,7 +106,7 @@ __device__ __forceinline__ void store_row(T* p, int t0, int end, const float (&v
 }
 
 template <class T, int TI, Part PART>
-__global__ __launch_bounds__(256) void scan_prompt(const sc_selective_scan a, const Split sp) {
+__global__ __launch_bounds__(256, 4) void scan_prompt(const sc_selective_scan a, const Split sp) {
   constexpr int CH = 16 * TI;                    // positions per chunk
   constexpr int MATS = PART == kEnds ? 1 : 2;    // b, and c where outputs are wanted
   extern __shared__ float lds[];
@@ -198,10 +211,7 @@ __global__ __launch_bounds__(256) void scan_prompt(const sc_selective_scan a, co
             S = fmaf(av[i], S, bv[i]);
           }
         }
-        compose<1>(P, S);
-        compose<2>(P, S);
-        compose<4>(P, S);
-        compose<8>(P, S);
+        compose16(P, S);
         if (PART != kEnds) {
           float h = fmaf(row_shr<1>(1.0f, P), Ah.y, row_shr<1>(0.0f, S));
 #pragma unroll
