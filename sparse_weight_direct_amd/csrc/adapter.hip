@@ -19,29 +19,6 @@ __device__ __forceinline__ int adapter_of(const sc_adapter& a, int b) {
   return r >= 0 && r < a.adapters ? r : -1;
 }
 
-// V values at p of which the first n exist; the others are 0 and not read.
-template <class T, int V>
-__device__ __forceinline__ typename Pack<T, V>::type load_some(const T* p, int n) {
-  typedef typename Pack<T, V>::type Vec;
-  if (n >= V) return *reinterpret_cast<const Vec*>(p);
-  Vec v;
-#pragma unroll
-  for (int i = 0; i < V; i++) v[i] = i < n ? p[i] : T(0.0f);
-  return v;
-}
-
-template <class T, int V>
-__device__ __forceinline__ void store_some(T* p, int n, typename Pack<T, V>::type v) {
-  typedef typename Pack<T, V>::type Vec;
-  if (n >= V) {
-    *reinterpret_cast<Vec*>(p) = v;
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; i++)
-      if (i < n) p[i] = v[i];
-  }
-}
-
 // ---- Prompts: two products on the matrix cores around R values a position.
 //
 // Both products have 16 rows of weights as one operand and positions as the other.  A lane loads

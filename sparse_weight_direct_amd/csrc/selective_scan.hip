@@ -6,7 +6,6 @@
 #include <algorithm>
 
 #include "sequence_device.h"
-#include "xcd.h"
 
 namespace sc {
 
@@ -15,31 +14,28 @@ namespace {
 // ---- Prompts
 //
 // The steps h -> a h + v of one state compose: two segments (P1, S1), (P2, S2), each its product
-// of a's and its end state from 0, make (P1 P2, P2 S1 + S2).  Sixteen lanes hold TI consecutive
-// positions each of one channel; a lane walks its positions once for (P, S), the sixteen are
-// scanned by row shifts (DPP, 4 steps), and the lane walks again from the state it now knows,
-// adding c h to its outputs, which stay in registers over all states n.  P needs no product over
-// the positions: it is exp(A sum s).
+// of a's and its end state from 0, make (P1 P2, P2 S1 + S2).  Sixteen lanes (a DPP row) hold TI
+// consecutive positions each of one channel; a lane walks its positions once for (P, S), the
+// sixteen are scanned by row shifts, and the lane walks again from the state it now knows, adding
+// c h to its outputs, which stay in registers over all states n.  P needs no product over the
+// positions: it is exp(A sum s).  Per (position, channel, state): 1 exp2, 2 products and 3 FMAs.
 //
-// A workgroup takes 16 channels of one group (4 a wavefront) and all its positions, 16 TI at a
-// time, so one copy of b and c in LDS (fp32, kStates states at a time) serves 16 channels.
-// Per (position, channel, state): 1 exp2, 2 products and 3 FMAs, and the scan's 20 instructions
-// shared by TI positions.
+// A workgroup takes 16 channels of one group (4 a wavefront) and walks its positions, 16 TI at a
+// time, with one copy of b and c in LDS (fp32, kStates states at a time): the four channels of a
+// wavefront read the same addresses.  Where there are few channels the axis is cut in segments: a
+// first pass makes each segment's end state from 0 (no outputs, no c), the second composes the
+// ends before its segment and walks it.
 
-constexpr int kRows = 16;     // channels per workgroup
-constexpr int kStates = 16;   // states of b and c in LDS at a time
+constexpr int kRows = 16;    // channels per workgroup
+constexpr int kStates = 16;  // states of b and c in LDS at a time
 
-// Pitch of a channel's {A, h} in LDS: one past N, so that the four channels of a wavefront read other
-// banks; at N = 256 none, which keeps the workgroup at 64 KB.
-__host__ __device__ constexpr int ah_pitch(int N) { return N < 256 ? N + 1 : 256; }
-
-enum Part { kWhole, kEnds, kSegment };
+// Pitch of a channel's {A, h} in LDS: one past N, so that the four channels of a wavefront read other banks.
+__host__ __device__ constexpr int ah_pitch(int N) { return N + 1; }
 
 struct Split {
-  int chunks;     // 16 TI positions each, per segment
-  int segments;
-  float* state;   // [B][segments][D][N]: entry 0 the initial state, entry s the end of segment s-1 from 0
-  float* sum;     // [B][segments][D]: entry s the sum of segment s-1's steps
+  int segments, chunks;  // segments of so many chunks of 16 TI positions
+  float* state;  // [B][segments][D][N]: entry 0 the initial state, entry s the end of segment s-1 from 0
+  float* sum;    // [B][segments][D]: entry s the sum of segment s-1's steps
 };
 
 template <int SHIFT>
@@ -50,25 +46,17 @@ __device__ __forceinline__ float row_shr(float old, float v) {
 
 // Inclusive scan of (P, S) over the sixteen lanes of a DPP row.  A lane without a source 1, 2, 4 or 8
 // lanes below keeps its values (its write is disabled), which is the identity step, so the shifts
-// need no constants: 8 instructions and the wait states between a write and its DPP read.
+// need no constants: 8 instructions, and the two wait states between a write and its DPP read.
 __device__ __forceinline__ void compose16(float& P, float& S) {
-  asm("s_nop 1\n\t"
-      "v_fmac_f32_dpp %1, %1, %0 row_shr:1 row_mask:0xf bank_mask:0xf\n\t"
-      "v_mul_f32_dpp %0, %0, %0 row_shr:1 row_mask:0xf bank_mask:0xf\n\t"
-      "s_nop 1\n\t"
-      "v_fmac_f32_dpp %1, %1, %0 row_shr:2 row_mask:0xf bank_mask:0xf\n\t"
-      "v_mul_f32_dpp %0, %0, %0 row_shr:2 row_mask:0xf bank_mask:0xf\n\t"
-      "s_nop 1\n\t"
-      "v_fmac_f32_dpp %1, %1, %0 row_shr:4 row_mask:0xf bank_mask:0xf\n\t"
-      "v_mul_f32_dpp %0, %0, %0 row_shr:4 row_mask:0xf bank_mask:0xf\n\t"
-      "s_nop 1\n\t"
-      "v_fmac_f32_dpp %1, %1, %0 row_shr:8 row_mask:0xf bank_mask:0xf\n\t"
-      "v_mul_f32_dpp %0, %0, %0 row_shr:8 row_mask:0xf bank_mask:0xf\n\t"
-      "s_nop 1"
-      : "+v"(P), "+v"(S));
+#define SCAN_STEP(d)                                                       \
+  "s_nop 1\n\t"                                                            \
+  "v_fmac_f32_dpp %1, %1, %0 row_shr:" d " row_mask:0xf bank_mask:0xf\n\t" \
+  "v_mul_f32_dpp %0, %0, %0 row_shr:" d " row_mask:0xf bank_mask:0xf\n\t"
+  asm(SCAN_STEP("1") SCAN_STEP("2") SCAN_STEP("4") SCAN_STEP("8") "s_nop 1" : "+v"(P), "+v"(S));
+#undef SCAN_STEP
 }
 
-// TI values of a row from position t0 on; those at or past `end` are 0 and not read.
+// TI values of a row from position t0 on, as fp32; those at or past `end` are 0 and not read.
 template <class T, int TI>
 __device__ __forceinline__ void load_row(const T* p, int t0, int end, float (&v)[TI]) {
   constexpr int V = TI * sizeof(T) >= 16 ? 16 / sizeof(T) : TI;
@@ -90,46 +78,45 @@ template <class T, int TI>
 __device__ __forceinline__ void store_row(T* p, int t0, int end, const float (&v)[TI]) {
   constexpr int V = TI * sizeof(T) >= 16 ? 16 / sizeof(T) : TI;
   typedef typename Pack<T, V>::type Vec;
-  if (t0 + TI <= end) {
 #pragma unroll
-    for (int i = 0; i < TI; i += V) {
-      Vec w;
+  for (int i = 0; i < TI; i += V) {
+    Vec w;
 #pragma unroll
-      for (int j = 0; j < V; j++) w[j] = T(v[i + j]);
-      *reinterpret_cast<Vec*>(p + t0 + i) = w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < TI; i++)
-      if (t0 + i < end) p[t0 + i] = T(v[i]);
+    for (int j = 0; j < V; j++) w[j] = T(v[i + j]);
+    store_some<T, V>(p + t0 + i, end - t0 - i, w);
   }
 }
 
-template <class T, int TI, Part PART>
+template <class T, int TI, bool ENDS>
 __global__ __launch_bounds__(256, 4) void scan_prompt(const sc_selective_scan a, const Split sp) {
-  constexpr int CH = 16 * TI;                    // positions per chunk
-  constexpr int MATS = PART == kEnds ? 1 : 2;    // b, and c where outputs are wanted
+  constexpr int CH = 16 * TI;         // positions per chunk
+  constexpr int MATS = ENDS ? 1 : 2;  // b, and c where outputs are wanted
+  constexpr int PIECES = MATS * kStates * CH / 8;  // of 8 positions of one state
   extern __shared__ float lds[];
-  float4* bc = reinterpret_cast<float4*>(lds);                              // [MATS][kStates][TI/4][16] quads of positions
-  float2* ah = reinterpret_cast<float2*>(lds + MATS * kStates * CH);        // [kRows][ah_pitch(N)]: {A log2(e), h}
+  // A chunk's positions lie in LDS as [TI/4][16 lanes][4]: a lane's quads are 16 bytes and neighbouring
+  // lanes' quads adjacent.
+  float4* bc = reinterpret_cast<float4*>(lds);                        // [MATS][kStates][CH/4]
+  float2* ah = reinterpret_cast<float2*>(lds + MATS * kStates * CH);  // [kRows + 1][ah_pitch(N)]: {A log2(e), h}
   const int tid = threadIdx.x, lane = tid & 15, row = tid >> 4;
   const int share = a.D / a.G, tiles = (share + kRows - 1) / kRows;
-  const int segments = PART == kWhole ? 1 : PART == kEnds ? sp.segments - 1 : sp.segments;
-  int id = xcd_logical(blockIdx.x, gridDim.x);
+  const int segments = ENDS ? sp.segments - 1 : sp.segments;
+  // neighbouring workgroups stay on different XCDs: sequences differ in length, and b and c are small
+  int id = blockIdx.x;
   const int tile = id % tiles;
   id /= tiles;
   const int seg = id % segments;
   id /= segments;
   const int g = id % a.G, b = id / a.G;
-  const int in_group = tile * kRows + row;
-  const bool live = in_group < share;
-  const int d = g * share + min(in_group, share - 1);
+  const bool live = tile * kRows + row < share;
+  const int d = g * share + min(tile * kRows + row, share - 1);
   const int slot = slot_of(a.slots, a.num_slots, b);
   const int len = slot < 0 ? 0 : length_of(a.lengths, a.L, b);
   const int N = a.N, AH = ah_pitch(N);
   const T* x = static_cast<const T*>(a.x) + b * a.x_batch + d * a.x_channel;
   const T* dt = static_cast<const T*>(a.dt) + b * a.dt_batch + d * a.dt_channel;
-  const T* z = a.z ? static_cast<const T*>(a.z) + b * a.z_batch + d * a.z_channel : nullptr;
+  const T* z = !ENDS && a.z ? static_cast<const T*>(a.z) + b * a.z_batch + d * a.z_channel : nullptr;
+  const T* bm = static_cast<const T*>(a.b) + b * a.b_batch + g * a.b_group;
+  const T* cm = static_cast<const T*>(a.c) + b * a.c_batch + g * a.c_group;
   T* out = static_cast<T*>(a.out) + b * a.out_batch + d * a.out_channel;
   const float skip = a.skip ? a.skip[d] : 0.0f, bias = a.dt_bias ? a.dt_bias[d] : 0.0f;
   const bool soft = a.flags & SC_SEQ_SOFTPLUS;
@@ -138,40 +125,44 @@ __global__ __launch_bounds__(256, 4) void scan_prompt(const sc_selective_scan a,
   for (int n = lane; n < N; n += 16) {
     const float A = a.A[(int64_t)d * N + n] * kLog2e;
     float h = 0.0f;
-    if (PART == kSegment) {
+    if (!ENDS && sp.segments > 1) {
       const float* st = sp.state + (((int64_t)b * sp.segments) * a.D + d) * N + n;
       const float* sm = sp.sum + (int64_t)b * sp.segments * a.D + d;
       h = st[0];
       for (int s = 1; s <= seg; s++) h = fmaf(exp2_fast(A * sm[(int64_t)s * a.D]), h, st[(int64_t)s * a.D * N]);
-    } else if (a.initial_state && slot >= 0 && (PART == kWhole || seg == 0)) {
+    } else if (a.initial_state && slot >= 0 && seg == 0) {
       h = a.initial_state[slot * a.initial_stride + (int64_t)d * N + n];
     }
-    if (PART == kEnds) {
+    if (ENDS) {
+      // the initial state goes to the workspace first: the second pass may overwrite it in place
       if (seg == 0 && live) sp.state[(((int64_t)b * sp.segments) * a.D + d) * N + n] = h;
       h = 0.0f;
     }
     ah[row * AH + n] = make_float2(A, h);
   }
+  // a DPP row's last lane has a chunk's end state; the others write theirs to a spare row
+  float* const carry = &ah[(lane == 15 ? row : kRows) * AH].y;
 
-  const int first = PART == kWhole ? 0 : seg * sp.chunks * CH;
-  const int last = PART == kWhole ? a.L : min(a.L, first + sp.chunks * CH);
+  const int first = seg * sp.chunks * CH;
+  const int last = sp.segments == 1 ? a.L : min(a.L, first + sp.chunks * CH);
+  const int walk = min(last, len);  // nothing of the sequence lies past it
   float total = 0.0f;
-  for (int c0 = first; c0 < last; c0 += CH) {
+  for (int c0 = first; c0 < walk; c0 += CH) {
     const int t0 = c0 + lane * TI;
+    const bool whole = c0 + CH <= len;
     float s[TI], sx[TI], y[TI], sum = 0.0f;
-    if (c0 >= len) {  // nothing of the sequence is left (the same for the whole workgroup)
-      if (PART == kEnds) break;
-#pragma unroll
-      for (int i = 0; i < TI; i++) y[i] = 0.0f;
-      if (live) store_row<T, TI>(out, t0, a.L, y);
-      continue;
-    }
     load_row<T, TI>(x, t0, len, y);
     load_row<T, TI>(dt, t0, len, s);
 #pragma unroll
     for (int i = 0; i < TI; i++) {
       const float raw = s[i] + bias;
-      s[i] = t0 + i < len ? (soft ? softplus(raw) : raw) : 0.0f;
+      s[i] = soft ? softplus(raw) : raw;
+    }
+    if (!whole)
+#pragma unroll
+      for (int i = 0; i < TI; i++) s[i] = t0 + i < len ? s[i] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < TI; i++) {
       sx[i] = s[i] * y[i];
       y[i] *= skip;
       sum += s[i];
@@ -180,18 +171,17 @@ __global__ __launch_bounds__(256, 4) void scan_prompt(const sc_selective_scan a,
     for (int n0 = 0; n0 < N; n0 += kStates) {
       const int ns = min(kStates, N - n0);
       __syncthreads();
-      // b and c of these states: 8 positions a thread, 0 past the length
-      for (int i = tid; i < MATS * ns * (CH / 8); i += 256) {
-        const int q = i % (CH / 8), m = i / (CH / 8), n = m % ns, mat = m / ns;
-        const T* p = mat ? static_cast<const T*>(a.c) + b * a.c_batch + g * a.c_group + (n0 + n) * a.c_state
-                         : static_cast<const T*>(a.b) + b * a.b_batch + g * a.b_group + (n0 + n) * a.b_state;
+#pragma unroll
+      for (int k = 0; k < (PIECES + 255) / 256; k++) {
+        const int i = tid + 256 * k, q = i % (CH / 8), m = i / (CH / 8), n = m % kStates;
+        if (n >= ns || (PIECES % 256 && i >= PIECES)) continue;
+        const T* p = MATS == 2 && m >= kStates ? cm + (n0 + n) * a.c_state : bm + (n0 + n) * a.b_state;
         float v[8];
         load_row<T, 8>(p, c0 + q * 8, len, v);
-        float4* to = bc + (mat * kStates + n) * (CH / 4);
 #pragma unroll
         for (int j = 0; j < 2; j++) {
-          const int k = q * 2 + j;  // quad of the chunk: lane k / (TI/4)
-          to[(k % (TI / 4)) * 16 + k / (TI / 4)] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          const int w = q * 2 + j;  // quad of the chunk, of lane w / (TI/4)
+          bc[m * (CH / 4) + w % (TI / 4) * 16 + w / (TI / 4)] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
         }
       }
       __syncthreads();
@@ -208,11 +198,11 @@ __global__ __launch_bounds__(256, 4) void scan_prompt(const sc_selective_scan a,
             const int i = 4 * k + j;
             av[i] = exp2_fast(s[i] * Ah.x);
             bv[i] = sx[i] * w[j];
-            S = fmaf(av[i], S, bv[i]);
+            S = i ? fmaf(av[i], S, bv[i]) : bv[i];
           }
         }
         compose16(P, S);
-        if (PART != kEnds) {
+        if (!ENDS) {
           float h = fmaf(row_shr<1>(1.0f, P), Ah.y, row_shr<1>(0.0f, S));
 #pragma unroll
           for (int k = 0; k < TI / 4; k++) {
@@ -226,32 +216,38 @@ __global__ __launch_bounds__(256, 4) void scan_prompt(const sc_selective_scan a,
             }
           }
         }
-        if (lane == 15) ah[row * AH + n0 + n].y = fmaf(P, Ah.y, S);
+        carry[2 * (n0 + n)] = fmaf(P, Ah.y, S);
       }
     }
-    if (PART != kEnds && live) {
+    if (!ENDS && live) {
       if (z) {
-        float g8[TI];
-        load_row<T, TI>(z, t0, len, g8);
+        float gate[TI];
+        load_row<T, TI>(z, t0, len, gate);
 #pragma unroll
-        for (int i = 0; i < TI; i++) y[i] *= silu(g8[i]);
+        for (int i = 0; i < TI; i++) y[i] *= silu(gate[i]);
       }
+      if (!whole)
 #pragma unroll
-      for (int i = 0; i < TI; i++) y[i] = t0 + i < len ? y[i] : 0.0f;
+        for (int i = 0; i < TI; i++) y[i] = t0 + i < len ? y[i] : 0.0f;
       store_row<T, TI>(out, t0, a.L, y);
     }
   }
   __syncthreads();
   if (!live) return;
-  if (PART == kEnds) {
+  if (ENDS) {
     float* st = sp.state + (((int64_t)b * sp.segments + seg + 1) * a.D + d) * N;
     for (int n = lane; n < N; n += 16) st[n] = ah[row * AH + n].y;
 #pragma unroll
     for (int m = 8; m; m >>= 1) total += __shfl_xor(total, m);
     if (lane == 0) sp.sum[((int64_t)b * sp.segments + seg + 1) * a.D + d] = total;
-  } else if (a.final_state && slot >= 0 && seg == segments - 1) {
-    for (int n = lane; n < N; n += 16) a.final_state[slot * a.final_stride + (int64_t)d * N + n] = ah[row * AH + n].y;
+    return;
   }
+  // the rest of the row: 0
+  const float zero[TI] = {};
+  for (int t0 = (walk > first ? first + (walk - first + CH - 1) / CH * CH : first) + lane * TI; t0 < last; t0 += CH)
+    store_row<T, TI>(out, t0, a.L, zero);
+  if (a.final_state && slot >= 0 && seg == segments - 1)
+    for (int n = lane; n < N; n += 16) a.final_state[slot * a.final_stride + (int64_t)d * N + n] = ah[row * AH + n].y;
 }
 
 // ---- Single positions
@@ -326,7 +322,7 @@ int launch_token(const sc_selective_scan& a, hipStream_t st) {
   return (int)hipGetLastError();
 }
 
-// How a prompt's scan is cut: positions per lane, and segments of the axis where there are few rows.
+// How a prompt's scan is cut: positions per lane, and segments of the axis where there are few channels.
 struct Plan {
   int ti, chunks, segments;
   int64_t groups;  // workgroups of a segment
@@ -334,37 +330,39 @@ struct Plan {
 
 Plan plan_of(const sc_selective_scan& a, int cus) {
   Plan p;
-  p.ti = a.L <= 64 ? 4 : a.L <= 128 ? 8 : 16;
+  p.ti = a.L <= 64 ? 4 : a.L <= 128 || a.N > 239 ? 8 : 16;  // beyond 239 states 16 would pass 64 KB of LDS
   const int64_t share = a.D / a.G;
   p.groups = (int64_t)a.B * a.G * ((share + kRows - 1) / kRows);
   const int chunks = std::max(1, (a.L + 16 * p.ti - 1) / (16 * p.ti));
   int64_t want = 1;
-  if (p.groups < 2 * cus) want = (4 * cus + p.groups - 1) / p.groups;
+  if (p.groups < cus) want = (4 * cus + p.groups - 1) / p.groups;
   const int most = std::max(1, std::min(chunks / 2, 64));
   int segments = (int)std::min<int64_t>(want, most);
+  if (p.ti < 16) segments = 1;
   p.chunks = (chunks + segments - 1) / segments;
   p.segments = (chunks + p.chunks - 1) / p.chunks;
   return p;
 }
 
-template <class T, int TI, Part PART>
+template <class T, int TI, bool ENDS>
 int launch_part(const sc_selective_scan& a, const Plan& p, const Split& sp, hipStream_t st) {
-  const int lds = ((PART == kEnds ? 1 : 2) * kStates * 16 * TI + kRows * ah_pitch(a.N) * 2) * 4;
-  const int64_t blocks = p.groups * (PART == kWhole ? 1 : PART == kEnds ? p.segments - 1 : p.segments);
-  hipLaunchKernelGGL((scan_prompt<T, TI, PART>), dim3((unsigned)blocks), dim3(256), lds, st, a, sp);
+  const int lds = ((ENDS ? 1 : 2) * kStates * 16 * TI + (kRows + 1) * ah_pitch(a.N) * 2) * 4;
+  const int64_t blocks = p.groups * (ENDS ? p.segments - 1 : p.segments);
+  hipLaunchKernelGGL((scan_prompt<T, TI, ENDS>), dim3((unsigned)blocks), dim3(256), lds, st, a, sp);
   return (int)hipGetLastError();
 }
 
-template <class T, int TI>
+template <class T>
 int launch_prompt(const sc_selective_scan& a, const Plan& p, hipStream_t st) {
-  Split sp{};
-  if (p.segments == 1) return launch_part<T, TI, kWhole>(a, p, sp, st);
-  sp.chunks = p.chunks;
-  sp.segments = p.segments;
-  sp.state = static_cast<float*>(a.workspace);
-  sp.sum = sp.state + (int64_t)a.B * p.segments * a.D * a.N;
-  if (const int e = launch_part<T, TI, kEnds>(a, p, sp, st)) return e;
-  return launch_part<T, TI, kSegment>(a, p, sp, st);
+  Split sp{p.segments, p.chunks, nullptr, nullptr};
+  if (p.ti == 4) return launch_part<T, 4, false>(a, p, sp, st);
+  if (p.ti == 8) return launch_part<T, 8, false>(a, p, sp, st);
+  if (p.segments > 1) {
+    sp.state = static_cast<float*>(a.workspace);
+    sp.sum = sp.state + (int64_t)a.B * p.segments * a.D * a.N;
+    if (const int e = launch_part<T, 16, true>(a, p, sp, st)) return e;
+  }
+  return launch_part<T, 16, false>(a, p, sp, st);
 }
 
 template <class T>
@@ -376,10 +374,7 @@ int launch_type(const sc_selective_scan& a, int cus, hipStream_t st) {
     if (a.N <= 32) return launch_token<T, 8>(a, st);
     return launch_token<T, 16>(a, st);
   }
-  const Plan p = plan_of(a, cus);
-  if (p.ti == 4) return launch_prompt<T, 4>(a, p, st);
-  if (p.ti == 8) return launch_prompt<T, 8>(a, p, st);
-  return launch_prompt<T, 16>(a, p, st);
+  return launch_prompt<T>(a, plan_of(a, cus), st);
 }
 
 }  // namespace

@@ -13,6 +13,29 @@ struct Pack {
   typedef T type __attribute__((ext_vector_type(V), aligned(sizeof(T))));
 };
 
+// V values at p of which the first n exist; the others are 0 and not read.
+template <class T, int V>
+__device__ __forceinline__ typename Pack<T, V>::type load_some(const T* p, int n) {
+  typedef typename Pack<T, V>::type Vec;
+  if (n >= V) return *reinterpret_cast<const Vec*>(p);
+  Vec v;
+#pragma unroll
+  for (int i = 0; i < V; i++) v[i] = i < n ? p[i] : T(0.0f);
+  return v;
+}
+
+template <class T, int V>
+__device__ __forceinline__ void store_some(T* p, int n, typename Pack<T, V>::type v) {
+  typedef typename Pack<T, V>::type Vec;
+  if (n >= V) {
+    *reinterpret_cast<Vec*>(p) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i++)
+      if (i < n) p[i] = v[i];
+  }
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
