@@ -87,8 +87,75 @@ __global__ __launch_bounds__(256) void causal_conv_rows(const sc_causal_conv a) 
   }
 }
 
+// Single positions: a thread takes kC channels, whose states lie together.
+constexpr int kC = 4;
+
+template <class T, int K, bool SILU>
+__global__ __launch_bounds__(256) void causal_conv_token(const sc_causal_conv a, int per_row) {
+  typedef typename Pack<T, kC>::type Vec;
+  const uint32_t id = blockIdx.x * 256u + threadIdx.x;
+  const int b = id / (uint32_t)per_row, d = (id - (uint32_t)b * per_row) * kC;
+  if (b >= a.B) return;
+  const int slot = slot_of(a.slots, a.num_slots, b), n = a.D - d;
+  const bool on = slot >= 0 && length_of(a.lengths, 1, b) == 1;
+  const T* x = static_cast<const T*>(a.x) + b * a.x_batch + d * a.x_channel;
+  T* out = static_cast<T*>(a.out) + b * a.out_batch + d * a.out_channel;
+  Vec now;
+  if (a.x_channel == 1)
+    now = load_some<T, kC>(x, n);
+  else
+#pragma unroll
+    for (int i = 0; i < kC; i++) now[i] = i < n ? x[i * a.x_channel] : T(0.0f);
+  T u[kC][K];  // a channel's last K - 1 inputs, and the present one
+  const T* from = a.initial_state && slot >= 0 ? static_cast<const T*>(a.initial_state) + slot * a.initial_stride + (int64_t)d * (K - 1)
+                                               : nullptr;
+  const int held = n * (K - 1);
+#pragma unroll
+  for (int r = 0; r < K - 1; r++) {
+    const Vec v = load_some<T, kC>(from + r * kC, from ? held - r * kC : 0);
+#pragma unroll
+    for (int i = 0; i < kC; i++) u[(r * kC + i) / (K - 1)][(r * kC + i) % (K - 1)] = v[i];
+  }
+  Vec y;
+#pragma unroll
+  for (int i = 0; i < kC; i++) {
+    u[i][K - 1] = now[i];
+    const int c = min(d + i, a.D - 1);
+    float v = a.bias ? a.bias[c] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; k++) v = fmaf(a.weight[(int64_t)c * K + k], (float)u[i][k], v);
+    if (SILU) v = silu(v);
+    y[i] = T(on ? v : 0.0f);
+  }
+  if (a.out_channel == 1)
+    store_some<T, kC>(out, n, y);
+  else
+#pragma unroll
+    for (int i = 0; i < kC; i++)
+      if (i < n) out[i * a.out_channel] = y[i];
+  if (K > 1 && a.final_state && slot >= 0) {
+    T* to = static_cast<T*>(a.final_state) + slot * a.final_stride + (int64_t)d * (K - 1);
+#pragma unroll
+    for (int r = 0; r < K - 1; r++) {
+      Vec v;
+#pragma unroll
+      for (int i = 0; i < kC; i++) {
+        const int c = (r * kC + i) / (K - 1), k = (r * kC + i) % (K - 1);
+        v[i] = on ? u[c][k + 1] : u[c][k];
+      }
+      store_some<T, kC>(to + r * kC, held - r * kC, v);
+    }
+  }
+}
+
 template <class T, int K, bool SILU>
 int launch_one(const sc_causal_conv& a, hipStream_t st) {
+  if (a.L == 1) {
+    const int per_row = (a.D + kC - 1) / kC;
+    hipLaunchKernelGGL((causal_conv_token<T, K, SILU>), dim3((unsigned)(((int64_t)a.B * per_row + 255) / 256)), dim3(256), 0,
+                       st, a, per_row);
+    return (int)hipGetLastError();
+  }
   const int64_t n = (int64_t)a.B * a.D * std::max(1, (a.L + kV - 1) / kV);
   hipLaunchKernelGGL((causal_conv_rows<T, K, SILU>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, a);
   return (int)hipGetLastError();

@@ -253,72 +253,94 @@ __global__ __launch_bounds__(256, 4) void scan_prompt(const sc_selective_scan a,
 // ---- Single positions
 //
 // The states are all that counts: 8 N bytes a channel, read and written once.  Q lanes share a
-// channel, four states a lane and pass (one 16-byte load), and sum its output by row shifts.
+// channel, four states a lane and pass (one 16-byte load), and a thread has four channels' loads in
+// flight; b and c of its states serve all four.  Lane k of a quad makes channel k's step and gate,
+// which its quad reads by DPP, and stores its output.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  const int w = __builtin_bit_cast(int, v);
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(w, w, CTRL, 0xf, 0xf, false));
+}
+
+// Four values of which the first n exist, `stride` apart.
+template <class T>
+__device__ __forceinline__ void load_states(const T* p, int64_t stride, int n, float (&v)[4]) {
+  if (stride == 1) {
+    const auto w = load_some<T, 4>(p, n);
+#pragma unroll
+    for (int j = 0; j < 4; j++) v[j] = (float)w[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; j++) v[j] = j < n ? (float)p[j * stride] : 0.0f;
+  }
+}
+
 template <class T, int Q>
-__global__ __launch_bounds__(256) void scan_token(const sc_selective_scan a) {
+__global__ __launch_bounds__(256) void scan_token(const sc_selective_scan a, int blocks) {
+  constexpr int U = 4, CPP = 256 / Q;  // channels per thread; per workgroup and u
   typedef typename Pack<float, 4>::type F4;
-  const int64_t id = (int64_t)blockIdx.x * (256 / Q) + threadIdx.x / Q;
-  const int lane = threadIdx.x % Q;
-  const bool live = id < (int64_t)a.B * a.D;
-  const int64_t at = live ? id : (int64_t)a.B * a.D - 1;
-  const int b = at / a.D, d = at - (int64_t)b * a.D, g = d / (a.D / a.G);
+  const int q = threadIdx.x % Q, k = threadIdx.x & 3, p = threadIdx.x / Q;
+  const int share = a.D / a.G;
+  const int base = blockIdx.x % blocks * (U * CPP) + p, g = blockIdx.x / blocks % a.G, b = blockIdx.x / blocks / a.G;
   const int slot = slot_of(a.slots, a.num_slots, b);
-  const bool on = live && slot >= 0 && length_of(a.lengths, 1, b) == 1;
-  T* out = static_cast<T*>(a.out) + b * a.out_batch + d * a.out_channel;
+  const bool on = slot >= 0 && length_of(a.lengths, 1, b) == 1;
+  const int own = min(base + k * CPP, share - 1), d = g * share + own;
   const float x = (float)static_cast<const T*>(a.x)[b * a.x_batch + d * a.x_channel];
   const float raw = (float)static_cast<const T*>(a.dt)[b * a.dt_batch + d * a.dt_channel] + (a.dt_bias ? a.dt_bias[d] : 0.0f);
-  const float s = a.flags & SC_SEQ_SOFTPLUS ? softplus(raw) : raw;
-  const float sx = s * x;
+  const float gate = a.z ? (float)static_cast<const T*>(a.z)[b * a.z_batch + d * a.z_channel] : 0.0f;
+  const float skip = a.skip ? a.skip[d] : 0.0f;
   const T* bm = static_cast<const T*>(a.b) + b * a.b_batch + g * a.b_group;
   const T* cm = static_cast<const T*>(a.c) + b * a.c_batch + g * a.c_group;
-  const float* from = a.initial_state && slot >= 0 ? a.initial_state + slot * a.initial_stride + (int64_t)d * a.N : nullptr;
-  float* to = a.final_state && slot >= 0 && live ? a.final_state + slot * a.final_stride + (int64_t)d * a.N : nullptr;
-  const float* A = a.A + (int64_t)d * a.N;
-  float y = 0.0f;
-  for (int n0 = lane * 4; n0 < a.N; n0 += 4 * Q) {
-    const int ns = min(4, a.N - n0);
-    F4 h = {0.0f, 0.0f, 0.0f, 0.0f}, w = h;
-    if (ns == 4) {
-      w = *reinterpret_cast<const F4*>(A + n0);
-      if (from) h = *reinterpret_cast<const F4*>(from + n0);
-    } else {
+  const int64_t c0 = (int64_t)(g * share) * a.N;
+  const float* from = a.initial_state && slot >= 0 ? a.initial_state + slot * a.initial_stride + c0 : nullptr;
+  float* to = a.final_state && slot >= 0 ? a.final_state + slot * a.final_stride + c0 : nullptr;
+  const float s_own = a.flags & SC_SEQ_SOFTPLUS ? softplus(raw) : raw, sx_own = s_own * x;
+  const float s[U] = {dpp<0x00>(s_own), dpp<0x55>(s_own), dpp<0xaa>(s_own), dpp<0xff>(s_own)};
+  const float sx[U] = {dpp<0x00>(sx_own), dpp<0x55>(sx_own), dpp<0xaa>(sx_own), dpp<0xff>(sx_own)};
+  float y[U] = {};
+  for (int n0 = q * 4; n0 < a.N; n0 += 4 * Q) {
+    const int ns = a.N - n0;
+    F4 h[U], A[U];
+    float bv[4], cv[4];
 #pragma unroll
-      for (int j = 0; j < 3; j++)
-        if (j < ns) {
-          w[j] = A[n0 + j];
-          if (from) h[j] = from[n0 + j];
-        }
+    for (int u = 0; u < U; u++) {
+      const bool live = base + u * CPP < share;
+      const int64_t at = (int64_t)(live ? base + u * CPP : 0) * a.N + n0;
+      A[u] = load_some<float, 4>(a.A + c0 + at, ns);
+      h[u] = from ? load_some<float, 4>(from + at, ns) : F4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    if (on) {
+    load_states(bm + n0 * a.b_state, a.b_state, ns, bv);
+    load_states(cm + n0 * a.c_state, a.c_state, ns, cv);
 #pragma unroll
-      for (int j = 0; j < 4; j++)
-        if (j < ns) {
-          h[j] = fmaf(exp2_fast(s * (w[j] * kLog2e)), h[j], sx * (float)bm[(n0 + j) * a.b_state]);
-          y = fmaf((float)cm[(n0 + j) * a.c_state], h[j], y);
+    for (int u = 0; u < U; u++) {
+      if (on)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          h[u][j] = fmaf(exp2_fast(s[u] * (A[u][j] * kLog2e)), h[u][j], sx[u] * bv[j]);
+          y[u] = fmaf(cv[j], h[u][j], y[u]);
         }
-    }
-    if (to) {
-      if (ns == 4)
-        *reinterpret_cast<F4*>(to + n0) = h;
-      else
-#pragma unroll
-        for (int j = 0; j < 3; j++)
-          if (j < ns) to[n0 + j] = h[j];
+      if (to && base + u * CPP < share) store_some<float, 4>(to + (int64_t)(base + u * CPP) * a.N + n0, ns, h[u]);
     }
   }
+  // the sum over the channel's lanes, in every lane: neighbours in a quad, then quads, then halves of a row
 #pragma unroll
-  for (int m = Q / 2; m; m >>= 1) y += __shfl_xor(y, m);
-  if (lane == 0 && live) {
-    y = fmaf(a.skip ? a.skip[d] : 0.0f, x, y);
-    if (a.z) y *= silu((float)static_cast<const T*>(a.z)[b * a.z_batch + d * a.z_channel]);
-    *out = T(on ? y : 0.0f);
+  for (int u = 0; u < U; u++) {
+    y[u] += dpp<0xb1>(y[u]);
+    y[u] += dpp<0x4e>(y[u]);
+    if (Q >= 8) y[u] += dpp<0x141>(y[u]);
+    if (Q >= 16) y[u] += dpp<0x140>(y[u]);
+  }
+  if (q < U && base + k * CPP < share) {
+    float o = fmaf(skip, x, k == 0 ? y[0] : k == 1 ? y[1] : k == 2 ? y[2] : y[3]);
+    if (a.z) o *= silu(gate);
+    static_cast<T*>(a.out)[b * a.out_batch + d * a.out_channel] = T(on ? o : 0.0f);
   }
 }
 
 template <class T, int Q>
 int launch_token(const sc_selective_scan& a, hipStream_t st) {
-  const int64_t rows = (int64_t)a.B * a.D, per = 256 / Q;
-  hipLaunchKernelGGL((scan_token<T, Q>), dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, st, a);
+  const int per = 4 * (256 / Q), blocks = (a.D / a.G + per - 1) / per;
+  hipLaunchKernelGGL((scan_token<T, Q>), dim3((unsigned)((int64_t)a.B * a.G * blocks)), dim3(256), 0, st, a, blocks);
   return (int)hipGetLastError();
 }
 
@@ -368,8 +390,6 @@ int launch_prompt(const sc_selective_scan& a, const Plan& p, hipStream_t st) {
 template <class T>
 int launch_type(const sc_selective_scan& a, int cus, hipStream_t st) {
   if (a.L == 1) {
-    if (a.N <= 4) return launch_token<T, 1>(a, st);
-    if (a.N <= 8) return launch_token<T, 2>(a, st);
     if (a.N <= 16) return launch_token<T, 4>(a, st);
     if (a.N <= 32) return launch_token<T, 8>(a, st);
     return launch_token<T, 16>(a, st);
