@@ -51,42 +51,40 @@ __device__ __forceinline__ F4 mfma(Tile<float>::KVec a, Tile<float>::KVec b, F4 
   return acc;
 }
 
-// low[seg][b][r][l] = scale sum over the segment's c of down[r][c] x[b][c][l], fp32.  Four wavefronts
-// take every fourth block of 4 K channels and add up in LDS, in order.
-template <class T, int RT>
-__global__ __launch_bounds__(256) void adapter_down(const sc_adapter a, float* low, int segments, int ltiles) {
+// A tile's lane starts at position l0 + V col, or where its V positions would pass the row's end at
+// L - V: every access is whole, and what two lanes then share only the first of them stores.  (L >= V.)
+__device__ __forceinline__ int lane_start(int l0, int V, int col, int L) { return min(l0 + V * col, L - V); }
+
+// low[seg][b][r][l] = scale sum over the segment's c of down[r][c] x[b][c][l], fp32.  NW wavefronts
+// take every NW-th block of 4 K channels; their sums are added in LDS, in order.
+template <class T, int RT, int NW>
+__global__ __launch_bounds__(64 * NW) void adapter_down(const sc_adapter a, float* low, int segments, int ltiles, int rpieces) {
   typedef Tile<T> X;
   typedef typename X::Vec Vec;
   typedef typename X::KVec KVec;
-  __shared__ float sum[RT * 16][X::L];
+  __shared__ float sum[NW][16][X::L];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, part = lane >> 4;
   int id = xcd_logical(blockIdx.x, gridDim.x);
   const int l0 = id % ltiles * X::L;
   id /= ltiles;
+  const int r0 = id % rpieces * (16 * RT);
+  id /= rpieces;
   const int seg = id % segments, b = id / segments;
   const int ad = adapter_of(a, b);
   if (ad < 0) return;
   const int blocks = (a.C + 4 * X::K - 1) / (4 * X::K), per = (blocks + segments - 1) / segments;
   const int end = min(blocks, (seg + 1) * per);
-  const T* w = static_cast<const T*>(a.down) + (int64_t)ad * a.R * a.C;
-  const int l = l0 + X::V * col, nl = a.L - l;
-  const T* x = static_cast<const T*>(a.x) + b * a.x_batch + l;
+  const T* x = static_cast<const T*>(a.x) + b * a.x_batch + lane_start(l0, X::V, col, a.L);
+  const T* w[RT];  // rows past R repeat the last one, and their sums are dropped
+#pragma unroll
+  for (int t = 0; t < RT; t++)
+    w[t] = static_cast<const T*>(a.down) + ((int64_t)ad * a.R + min(r0 + t * 16 + col, a.R - 1)) * a.C;
   F4 acc[RT][X::V];
 #pragma unroll
   for (int t = 0; t < RT; t++)
 #pragma unroll
     for (int q = 0; q < X::V; q++) acc[t][q] = F4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int blk = seg * per + wave; blk < end; blk += 4) {
-    const int c = blk * 4 * X::K + part * X::K, nc = a.C - c;
-    Vec xv[X::K];
-    KVec wv[RT];
-#pragma unroll
-    for (int i = 0; i < X::K; i++) xv[i] = load_some<T, X::V>(x + (int64_t)(c + i) * a.x_channel, i < nc ? nl : 0);
-#pragma unroll
-    for (int t = 0; t < RT; t++) {
-      const int r = t * 16 + col;
-      wv[t] = load_some<T, X::K>(w + (int64_t)r * a.C + c, r < a.R ? nc : 0);
-    }
+  auto product = [&](const Vec(&xv)[X::K], const KVec(&wv)[RT]) {
 #pragma unroll
     for (int q = 0; q < X::V; q++) {
       KVec xq;
@@ -95,43 +93,73 @@ __global__ __launch_bounds__(256) void adapter_down(const sc_adapter a, float* l
 #pragma unroll
       for (int t = 0; t < RT; t++) acc[t][q] = mfma(wv[t], xq, acc[t][q]);
     }
+  };
+  int blk = seg * per + wave;
+  const int whole = min(end, a.C / (4 * X::K));
+#pragma unroll 2
+  for (; blk < whole; blk += NW) {
+    const int c = blk * 4 * X::K + part * X::K;
+    Vec xv[X::K];
+    KVec wv[RT];
+#pragma unroll
+    for (int i = 0; i < X::K; i++) xv[i] = *reinterpret_cast<const Vec*>(x + (c + i) * a.x_channel);
+#pragma unroll
+    for (int t = 0; t < RT; t++) wv[t] = *reinterpret_cast<const KVec*>(w[t] + c);
+    product(xv, wv);
   }
-  for (int k = 0; k < 4; k++) {
-    if (wave == k)
+  if (blk < end) {  // the last channels: zeros in both operands
+    const int c = blk * 4 * X::K + part * X::K, nc = a.C - c;
+    Vec xv[X::K];
+    KVec wv[RT];
 #pragma unroll
-      for (int t = 0; t < RT; t++)
+    for (int i = 0; i < X::K; i++) xv[i] = load_some<T, X::V>(x + (c + i) * a.x_channel, i < nc ? X::V : 0);
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-#pragma unroll
-          for (int q = 0; q < X::V; q++) {
-            float& s = sum[t * 16 + part * 4 + i][X::V * col + q];
-            s = k ? s + acc[t][q][i] : acc[t][q][i];
-          }
-    __syncthreads();
+    for (int t = 0; t < RT; t++) wv[t] = load_some<T, X::K>(w[t] + c, nc);
+    product(xv, wv);
   }
   const float scale = a.scale ? a.scale[ad] : 1.0f;
   float* to = low + ((int64_t)seg * a.B + b) * a.R * a.L;
-  for (int i = threadIdx.x; i < a.R * X::L; i += 256) {
-    const int r = i / X::L, j = i % X::L;
-    if (l0 + j < a.L) to[(int64_t)r * a.L + l0 + j] = scale * sum[r][j];
+#pragma unroll
+  for (int t = 0; t < RT; t++) {
+    if (t) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+      for (int q = 0; q < X::V; q += 4)
+        *reinterpret_cast<F4*>(&sum[wave][part * 4 + i][X::V * col + q]) =
+            F4{acc[t][q][i], acc[t][q + 1][i], acc[t][q + 2][i], acc[t][q + 3][i]};
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * X::L; i += 64 * NW) {
+      const int r = i / X::L, j = i % X::L;
+      float v = 0.0f;
+#pragma unroll
+      for (int k = 0; k < NW; k++) v += sum[k][r][j];
+      const int own = l0 + j / X::V * X::V, l = lane_start(l0, X::V, j / X::V, a.L) + j % X::V;
+      if (r0 + t * 16 + r < a.R && l >= own) to[(int64_t)(r0 + t * 16 + r) * a.L + l] = scale * v;
+    }
   }
 }
 
-// The sum over the segments of 8 rows of low from r0 on, at one position; 0 past R.
+// The sum over the segments of 8 rows of low from r0 on, at one position; 0 past R (where the last row is
+// read instead: no branch stands between the loads).
 __device__ __forceinline__ void low_rows(const sc_adapter& a, const float* low, int segments, int b, int r0, int l,
                                          float (&v)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    v[i] = 0.0f;
-    if (r0 + i < a.R && l < a.L)
-      for (int s = 0; s < segments; s++) v[i] += low[(((int64_t)s * a.B + b) * a.R + r0 + i) * a.L + l];
+  for (int i = 0; i < 8; i++) v[i] = 0.0f;
+  for (int s = 0; s < segments; s++) {
+    const float* p = low + ((int64_t)s * a.B + b) * a.R * a.L + l;
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] += p[(int64_t)min(r0 + i, a.R - 1) * a.L];
   }
+#pragma unroll
+  for (int i = 0; i < 8; i++) v[i] = r0 + i < a.R ? v[i] : 0.0f;
 }
 
 // out = base + up low for `mrows` output channels of one tile of positions.  low is held in LDS as the
 // matrix cores take it: fp32 as it is; for 16-bit types as the sum of two 16-bit values, which share
 // one instruction (its 32 summed rows are 16 high parts and the same 16 low parts), so the
 // intermediate keeps 16 bits.  fp16's narrow exponent is met by a power of two per position.
+// The next 16 channels' base is on its way while these are computed and stored.
 template <class T>
 __global__ __launch_bounds__(256) void adapter_up(const sc_adapter a, const float* low, int segments, int ltiles,
                                                   int mtiles, int mrows) {
@@ -142,9 +170,9 @@ __global__ __launch_bounds__(256) void adapter_up(const sc_adapter a, const floa
   constexpr bool kWide = sizeof(T) == 4;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, part = lane >> 4;
   int id = xcd_logical(blockIdx.x, gridDim.x);
-  const int m_begin = id % mtiles * mrows;
-  id /= mtiles;
-  const int l0 = id % ltiles * X::L, b = id / ltiles;
+  const int l0 = id % ltiles * X::L;
+  id /= ltiles;
+  const int m_begin = id % mtiles * mrows, b = id / mtiles;
   const int ad = adapter_of(a, b);
   const int R16 = (a.R + 15) / 16;
   float back[X::V];  // 2^e of the lane's positions
@@ -155,21 +183,21 @@ __global__ __launch_bounds__(256) void adapter_up(const sc_adapter a, const floa
       for (int i = tid; i < R16 * 2 * X::L; i += 256) {
         const int j = i % X::L, r0 = i / X::L * 8;
         float v[8];
-        low_rows(a, low, segments, b, r0, l0 + j, v);
+        low_rows(a, low, segments, b, r0, lane_start(l0, X::V, j / X::V, a.L) + j % X::V, v);
 #pragma unroll
         for (int k = 0; k < 8; k++) lds[(r0 + k) * X::L + j] = v[k];
       }
       __syncthreads();
     } else {
       // two threads a position, each with every other 8 rows
-      const int j = tid & 127, half = tid >> 7;
+      const int j = tid & 127, half = tid >> 7, at = lane_start(l0, X::V, j / X::V, a.L) + j % X::V;
       float forth = 1.0f;
       if constexpr (__is_same(T, _Float16)) {
         float* most = lds;  // [2][128], before the operands take the place
         float m = 0.0f;
         for (int k = 0; k < R16; k++) {
           float v[8];
-          low_rows(a, low, segments, b, k * 16 + half * 8, l0 + j, v);
+          low_rows(a, low, segments, b, k * 16 + half * 8, at, v);
 #pragma unroll
           for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(v[i]));
         }
@@ -189,7 +217,7 @@ __global__ __launch_bounds__(256) void adapter_up(const sc_adapter a, const floa
       KVec* op = reinterpret_cast<KVec*>(lds);  // [R16][8 tiles][64 lanes]
       for (int k = 0; k < R16; k++) {
         float v[8];
-        low_rows(a, low, segments, b, k * 16 + half * 8, l0 + j, v);
+        low_rows(a, low, segments, b, k * 16 + half * 8, at, v);
         KVec hi, lo;
 #pragma unroll
         for (int i = 0; i < 8; i++) {
@@ -206,26 +234,33 @@ __global__ __launch_bounds__(256) void adapter_up(const sc_adapter a, const floa
     }
   }
   const T* w = static_cast<const T*>(a.up) + (int64_t)max(ad, 0) * a.M * a.R;
-  const int l = l0 + X::V * col, nl = a.L - l;
+  const int own = l0 + X::V * col, l = lane_start(l0, X::V, col, a.L);
   const T* base = static_cast<const T*>(a.base);
   if (base) base += b * a.base_batch + l;
   T* out = static_cast<T*>(a.out) + b * a.out_batch + l;
   const int m_end = min(a.M, m_begin + mrows);
-  for (int m0 = m_begin + wave * 16; m0 < m_end; m0 += 64) {
+  Vec next[4] = {};
+  auto fetch = [&](int m0) {
+    if (base)
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        next[i] = *reinterpret_cast<const Vec*>(base + min(m0 + part * 4 + i, m_end - 1) * a.base_channel);
+  };
+  int m0 = m_begin + wave * 16;
+  if (m0 < m_end) fetch(m0);
+  for (; m0 < m_end; m0 += 64) {
     Vec bv[4];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int m = m0 + part * 4 + i;
-      bv[i] = load_some<T, X::V>(base + (int64_t)m * a.base_channel, base && m < m_end ? nl : 0);
-    }
+    for (int i = 0; i < 4; i++) bv[i] = next[i];
+    if (m0 + 64 < m_end) fetch(m0 + 64);
     F4 acc[X::V];
 #pragma unroll
     for (int q = 0; q < X::V; q++) acc[q] = F4{0.0f, 0.0f, 0.0f, 0.0f};
     if (ad >= 0) {
-      const int m = m0 + col;
+      const T* wm = w + (int64_t)min(m0 + col, m_end - 1) * a.R;
       for (int k = 0; k < R16; k++) {
         const int r = k * 16 + (kWide ? part * 4 : (part & 1) * 8);
-        const KVec wv = load_some<T, X::K>(w + (int64_t)m * a.R + r, m < m_end ? a.R - r : 0);
+        const KVec wv = k * 16 + 16 <= a.R ? *reinterpret_cast<const KVec*>(wm + r) : load_some<T, X::K>(wm + r, a.R - r);
         if constexpr (kWide) {
           F4 lv[4];
 #pragma unroll
@@ -245,19 +280,30 @@ __global__ __launch_bounds__(256) void adapter_up(const sc_adapter a, const floa
       Vec v;
 #pragma unroll
       for (int q = 0; q < X::V; q++) v[q] = T(fmaf(acc[q][i], back[q], (float)bv[i][q]));
-      if (m < m_end) store_some<T, X::V>(out + (int64_t)m * a.out_channel, nl, v);
+      if (m >= m_end) continue;
+      T* to = out + m * a.out_channel;
+      if (l == own) {
+        *reinterpret_cast<Vec*>(to) = v;
+      } else {
+#pragma unroll
+        for (int q = 0; q < X::V; q++)
+          if (l + q >= own) to[q] = v[q];
+      }
     }
   }
 }
 
 // ---- Single positions: one launch.  A workgroup takes one position's `mrows` output channels and
 // makes the R values for itself (down[r] comes from L2 after the first workgroup has read it), which
-// costs less than a second launch.
-constexpr int kToken = 512;
+// costs less than a second launch.  Its time is latency: what the second half needs (the base and the
+// first kFront values of every row of up) is asked for before the first half begins.
+constexpr int kToken = 512;   // threads
+constexpr int kTokenRows = 2;   // output channels per thread
+constexpr int kFront = 16;
 
 template <class T>
 __global__ __launch_bounds__(kToken) void adapter_token(const sc_adapter a, int mtiles, int mrows) {
-  constexpr int V = 16 / sizeof(T);
+  constexpr int V = 16 / sizeof(T), F = kFront / V;
   typedef typename Pack<T, V>::type Vec;
   __shared__ float low[128];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -266,73 +312,102 @@ __global__ __launch_bounds__(kToken) void adapter_token(const sc_adapter a, int 
   id /= mtiles;
   const int l = id % a.L, b = id / a.L;
   const int ad = adapter_of(a, b);
+  const T* up = static_cast<const T*>(a.up) + (int64_t)max(ad, 0) * a.M * a.R;
+  const T* base = a.base ? static_cast<const T*>(a.base) + b * a.base_batch + l : nullptr;
+  T first[kTokenRows];
+  Vec front[kTokenRows][F];
+#pragma unroll
+  for (int k = 0; k < kTokenRows; k++) {
+    const int m = min(mt * mrows + (int)threadIdx.x + k * kToken, a.M - 1);
+    first[k] = base ? base[m * a.base_channel] : T(0.0f);
+    if (ad < 0) continue;
+#pragma unroll
+    for (int f = 0; f < F; f++)
+      front[k][f] = f * V + V <= a.R ? *reinterpret_cast<const Vec*>(up + (int64_t)m * a.R + f * V)
+                                     : load_some<T, V>(up + (int64_t)m * a.R + f * V, a.R - f * V);
+  }
   if (ad >= 0) {
     const T* x = static_cast<const T*>(a.x) + b * a.x_batch + l;
     const T* w = static_cast<const T*>(a.down) + (int64_t)ad * a.R * a.C;
     const float scale = a.scale ? a.scale[ad] : 1.0f;
-    for (int r = wave; r < a.R; r += kToken / 64) {
-      const T* wr = w + (int64_t)r * a.C;
-      float v = 0.0f;
-      for (int c = lane * V; c < a.C; c += 64 * V) {
-        const int n = a.C - c;
-        const Vec wv = load_some<T, V>(wr + c, n);
-        Vec xv;
-        if (a.x_channel == 1) {
-          xv = load_some<T, V>(x + c, n);
-        } else {
+    auto x_at = [&](int c) {
+      if (a.x_channel == 1) return *reinterpret_cast<const Vec*>(x + c);
+      Vec v;
 #pragma unroll
-          for (int i = 0; i < V; i++) xv[i] = i < n ? x[(c + i) * a.x_channel] : T(0.0f);
-        }
+      for (int i = 0; i < V; i++) v[i] = x[(c + i) * a.x_channel];
+      return v;
+    };
+    // two rows at a time, four pieces of each in flight
+    for (int r = 2 * wave; r < a.R; r += 2 * (kToken / 64)) {
+      const T* w0 = w + (int64_t)r * a.C;
+      const T* w1 = w + (int64_t)min(r + 1, a.R - 1) * a.C;
+      float v0 = 0.0f, v1 = 0.0f;
+      int c = lane * V;
+#pragma unroll 4
+      for (; c + V <= a.C; c += 64 * V) {
+        const Vec xv = x_at(c), wv = *reinterpret_cast<const Vec*>(w0 + c), wu = *reinterpret_cast<const Vec*>(w1 + c);
 #pragma unroll
-        for (int i = 0; i < V; i++) v = fmaf((float)wv[i], (float)xv[i], v);
+        for (int i = 0; i < V; i++) v0 = fmaf((float)wv[i], (float)xv[i], v0), v1 = fmaf((float)wu[i], (float)xv[i], v1);
+      }
+      for (int i = c; i < a.C && i < c + V; i++) {
+        const float xv = (float)x[i * a.x_channel];
+        v0 = fmaf((float)w0[i], xv, v0), v1 = fmaf((float)w1[i], xv, v1);
       }
 #pragma unroll
-      for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
-      if (lane == 0) low[r] = scale * v;
+      for (int m = 32; m; m >>= 1) v0 += __shfl_xor(v0, m), v1 += __shfl_xor(v1, m);
+      if (lane == 0) {
+        low[r] = scale * v0;
+        if (r + 1 < a.R) low[r + 1] = scale * v1;
+      }
     }
   }
   __syncthreads();
-  const int m_end = min(a.M, (mt + 1) * mrows);
-  for (int m = mt * mrows + threadIdx.x; m < m_end; m += kToken) {
-    float v = a.base ? (float)static_cast<const T*>(a.base)[b * a.base_batch + m * a.base_channel + l] : 0.0f;
+#pragma unroll
+  for (int k = 0; k < kTokenRows; k++) {
+    const int m = mt * mrows + threadIdx.x + k * kToken;
+    if (m >= a.M) continue;
+    float s = 0.0f;
     if (ad >= 0) {
-      const T* w = static_cast<const T*>(a.up) + ((int64_t)ad * a.M + m) * a.R;
-      float s = 0.0f;
-      for (int r = 0; r < a.R; r += V) {
-        const Vec wv = load_some<T, V>(w + r, a.R - r);
+#pragma unroll
+      for (int r = 0; r < kFront; r++)
+        if (r < a.R) s = fmaf((float)front[k][r / V][r % V], low[r], s);
+      for (int r = kFront; r < a.R; r += V) {
+        const Vec wv = load_some<T, V>(up + (int64_t)m * a.R + r, a.R - r);
 #pragma unroll
         for (int i = 0; i < V; i++)
           if (r + i < a.R) s = fmaf((float)wv[i], low[r + i], s);
       }
-      v += s;
     }
-    static_cast<T*>(a.out)[b * a.out_batch + m * a.out_channel + l] = T(v);
+    static_cast<T*>(a.out)[b * a.out_batch + m * a.out_channel + l] = T((float)first[k] + s);
   }
 }
 
 struct Plan {
   bool token;
-  int ltiles, segments;  // positions' tiles; pieces of C
+  int ltiles, segments, rpieces;  // positions' tiles; pieces of C and of R
   int mtiles, mrows;     // output channels' pieces
 };
 
 Plan plan_of(const sc_adapter& a, int cus) {
   Plan p{};
   const bool wide = a.dtype == SC_F32;
-  p.token = a.L <= 4;
+  p.token = a.L < 8;  // the tiles' lanes hold 8 positions
   if (p.token) {
-    p.mtiles = (a.M + 2 * kToken - 1) / (2 * kToken);
-    p.mrows = (a.M + p.mtiles - 1) / p.mtiles;
+    p.mrows = kTokenRows * kToken;
+    p.mtiles = (a.M + p.mrows - 1) / p.mrows;
     return p;
   }
   p.ltiles = (a.L + (wide ? 64 : 128) - 1) / (wide ? 64 : 128);
   const int64_t tiles = (int64_t)a.B * p.ltiles;
   const int blocks = (a.C + (wide ? 16 : 32) - 1) / (wide ? 16 : 32);
-  p.segments = (int)std::clamp<int64_t>((2 * cus + tiles - 1) / tiles, 1, std::max(1, std::min(blocks / 8, 8)));
+  p.rpieces = (a.R + 63) / 64;
+  const int nw = a.R <= 32 ? 8 : 4;
+  p.segments = (int)std::clamp<int64_t>((2 * cus + tiles * p.rpieces - 1) / (tiles * p.rpieces), 1,
+                                        std::max(1, std::min(blocks / nw, 4)));
   // an empty last piece would leave its part of the workspace unwritten
   const int per = (blocks + p.segments - 1) / p.segments;
   p.segments = (blocks + per - 1) / per;
-  p.mtiles = (int)std::clamp<int64_t>((8 * cus + tiles - 1) / tiles, 1, (a.M + 63) / 64);
+  p.mtiles = (int)std::clamp<int64_t>((4 * cus + tiles - 1) / tiles, 1, (a.M + 127) / 128);
   p.mrows = ((a.M + p.mtiles - 1) / p.mtiles + 63) / 64 * 64;
   p.mtiles = (a.M + p.mrows - 1) / p.mrows;
   return p;
@@ -347,20 +422,18 @@ int launch_type(const sc_adapter& a, int cus, hipStream_t st) {
     return (int)hipGetLastError();
   }
   float* low = static_cast<float*>(a.workspace);
-  const int64_t nd = (int64_t)a.B * p.ltiles * p.segments, nu = (int64_t)a.B * p.ltiles * p.mtiles;
-  const dim3 gd((unsigned)nd), gu((unsigned)nu), block(256);
+  const int64_t nd = (int64_t)a.B * p.ltiles * p.segments * p.rpieces, nu = (int64_t)a.B * p.ltiles * p.mtiles;
+  const dim3 gd((unsigned)nd), gu((unsigned)nu);
   if (a.R <= 16)
-    hipLaunchKernelGGL((adapter_down<T, 1>), gd, block, 0, st, a, low, p.segments, p.ltiles);
+    hipLaunchKernelGGL((adapter_down<T, 1, 8>), gd, dim3(512), 0, st, a, low, p.segments, p.ltiles, p.rpieces);
   else if (a.R <= 32)
-    hipLaunchKernelGGL((adapter_down<T, 2>), gd, block, 0, st, a, low, p.segments, p.ltiles);
-  else if (a.R <= 64)
-    hipLaunchKernelGGL((adapter_down<T, 4>), gd, block, 0, st, a, low, p.segments, p.ltiles);
+    hipLaunchKernelGGL((adapter_down<T, 2, 8>), gd, dim3(512), 0, st, a, low, p.segments, p.ltiles, p.rpieces);
   else
-    hipLaunchKernelGGL((adapter_down<T, 8>), gd, block, 0, st, a, low, p.segments, p.ltiles);
+    hipLaunchKernelGGL((adapter_down<T, 4, 4>), gd, dim3(256), 0, st, a, low, p.segments, p.ltiles, p.rpieces);
   if (const int e = (int)hipGetLastError()) return e;
   const int R16 = (a.R + 15) / 16;
   const int lds = sizeof(T) == 4 ? R16 * 16 * 64 * 4 : R16 * 8 * 64 * 16;
-  hipLaunchKernelGGL((adapter_up<T>), gu, block, lds, st, a, low, p.segments, p.ltiles, p.mtiles, p.mrows);
+  hipLaunchKernelGGL((adapter_up<T>), gu, dim3(256), lds, st, a, low, p.segments, p.ltiles, p.mtiles, p.mrows);
   return (int)hipGetLastError();
 }
 
