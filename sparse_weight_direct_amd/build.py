@@ -11,6 +11,8 @@ PROBE_LIB = os.path.join(HERE, "libscprobe.so")  # roof probes timed by the benc
 PROBE_SOURCE = os.path.join(HERE, "csrc", "probes.hip")
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("kernels.hip", "escoin.hip", "dense.hip", "pack.cpp", "bake.cpp", "api.cpp",
                                                "causal_conv.hip", "selective_scan.hip", "adapter.hip", "sequence.cpp")]
+BINDING_LIB = os.path.join(HERE, "_binding.so")  # tensor arguments of the sequence operators
+BINDING_SOURCE = os.path.join(HERE, "csrc", "binding.cpp")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # Packed FP32 instructions are disabled for all device code: hipcc would otherwise form
@@ -24,6 +26,20 @@ def _run(cmd):
     res = subprocess.run(cmd, capture_output=True, text=True)
     out = "\n".join(l for l in (res.stdout + res.stderr).splitlines() if "packed-fp32-ops" not in l)
     return res.returncode, out
+
+
+def _binding_command(out):
+    """The host compiler's line for the binding: torch's headers and libraries, and libsparseconv.so beside it."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    inc = [f for d in include_paths() + [sysconfig.get_paths()["include"]] for f in ("-isystem", d)]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + inc + \
+           [BINDING_SOURCE, "-o", out, "-L" + lib, "-L" + HERE, "-l:libsparseconv.so", "-ltorch_python", "-ltorch_cpu", "-lc10",
+            "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
 
 
 def build(verbose: bool = False) -> str:
@@ -56,6 +72,11 @@ def build(verbose: bool = False) -> str:
     if rc != 0:
         raise RuntimeError(f"hipcc failed on probes.hip ({rc}):\n{out}")
     os.replace(tmp, PROBE_LIB)
+    tmp = BINDING_LIB + ".tmp"
+    rc, out = _run(_binding_command(tmp))
+    if rc != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp ({rc}):\n{out}")
+    os.replace(tmp, BINDING_LIB)
     return LIB
 
 
