@@ -87,8 +87,8 @@ __device__ __forceinline__ void store_row(T* p, int t0, int end, const float (&v
   }
 }
 
-template <class T, int TI, bool ENDS>
-__global__ __launch_bounds__(256, 4) void scan_prompt(const sc_selective_scan a, const Split sp) {
+template <class T, int TI, bool ENDS, bool AHEAD>
+__global__ __launch_bounds__(256, AHEAD ? 2 : 4) void scan_prompt(const sc_selective_scan a, const Split sp) {
   constexpr int CH = 16 * TI;         // positions per chunk
   constexpr int MATS = ENDS ? 1 : 2;  // b, and c where outputs are wanted
   constexpr int PIECES = MATS * kStates * CH / 8;  // of 8 positions of one state
@@ -146,13 +146,49 @@ __global__ __launch_bounds__(256, 4) void scan_prompt(const sc_selective_scan a,
   const int first = seg * sp.chunks * CH;
   const int last = sp.segments == 1 ? a.L : min(a.L, first + sp.chunks * CH);
   const int walk = min(last, len);  // nothing of the sequence lies past it
+
+  // AHEAD: the next pass's b and c and the next chunk's rows are on their way during the state loop,
+  // in registers and without a branch; only whole chunks are.
+  static_assert(!AHEAD || TI == 16, "");
+  typedef typename Pack<T, 8>::type Vec8;
+  constexpr int AR = AHEAD ? TI / 8 : 1, AP = AHEAD ? PIECES / 256 : 1;
+  Vec8 xr[AR], dr[AR], zr[AR], stage[AP];
+  auto take = [&](const T* p, Vec8(&r)[AR]) {
+#pragma unroll
+    for (int i = 0; i < AR; i++) r[i] = *reinterpret_cast<const Vec8*>(p + 8 * i);
+  };
+  auto fetch_rows = [&](int c0) {
+    if (c0 + CH > len) return;
+    take(x + c0 + lane * TI, xr);
+    take(dt + c0 + lane * TI, dr);
+  };
+  auto piece = [&](int i, int n0) {  // piece i of the states from n0 on: its first position's address
+    const int q = i % (CH / 8), m = i / (CH / 8), n = min(n0 + m % kStates, N - 1);
+    return (MATS == 2 && m >= kStates ? cm + n * a.c_state : bm + n * a.b_state) + q * 8;
+  };
+  auto fetch_bc = [&](int n0, int c0) {
+    if (c0 + CH > len) return;
+#pragma unroll
+    for (int k = 0; k < AP; k++) stage[k] = *reinterpret_cast<const Vec8*>(piece(tid + 256 * k, n0) + c0);
+  };
+  if (AHEAD && first < walk) {
+    fetch_rows(first);
+    fetch_bc(0, first);
+  }
   float total = 0.0f;
   for (int c0 = first; c0 < walk; c0 += CH) {
     const int t0 = c0 + lane * TI;
     const bool whole = c0 + CH <= len;
     float s[TI], sx[TI], y[TI], sum = 0.0f;
-    load_row<T, TI>(x, t0, len, y);
-    load_row<T, TI>(dt, t0, len, s);
+    if (AHEAD && whole) {
+#pragma unroll
+      for (int i = 0; i < TI; i++) y[i] = (float)xr[i / 8 % AR][i % 8], s[i] = (float)dr[i / 8 % AR][i % 8];
+      if (z) take(z + t0, zr);
+      if (c0 + CH < walk) fetch_rows(c0 + CH);
+    } else {
+      load_row<T, TI>(x, t0, len, y);
+      load_row<T, TI>(dt, t0, len, s);
+    }
 #pragma unroll
     for (int i = 0; i < TI; i++) {
       const float raw = s[i] + bias;
@@ -171,20 +207,36 @@ __global__ __launch_bounds__(256, 4) void scan_prompt(const sc_selective_scan a,
     for (int n0 = 0; n0 < N; n0 += kStates) {
       const int ns = min(kStates, N - n0);
       __syncthreads();
-#pragma unroll
-      for (int k = 0; k < (PIECES + 255) / 256; k++) {
-        const int i = tid + 256 * k, q = i % (CH / 8), m = i / (CH / 8), n = m % kStates;
-        if (n >= ns || (PIECES % 256 && i >= PIECES)) continue;
-        const T* p = MATS == 2 && m >= kStates ? cm + (n0 + n) * a.c_state : bm + (n0 + n) * a.b_state;
-        float v[8];
-        load_row<T, 8>(p, c0 + q * 8, len, v);
+      auto put = [&](int i, const float(&v)[8]) {
+        const int q = i % (CH / 8), m = i / (CH / 8);
 #pragma unroll
         for (int j = 0; j < 2; j++) {
           const int w = q * 2 + j;  // quad of the chunk, of lane w / (TI/4)
           bc[m * (CH / 4) + w % (TI / 4) * 16 + w / (TI / 4)] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
         }
+      };
+      float v[8];
+      if (AHEAD && whole) {
+#pragma unroll
+        for (int k = 0; k < AP; k++) {
+#pragma unroll
+          for (int j = 0; j < 8; j++) v[j] = (float)stage[k][j];
+          put(tid + 256 * k, v);
+        }
+      } else {
+#pragma unroll(AHEAD ? 1 : (PIECES + 255) / 256)
+        for (int k = 0; k < (PIECES + 255) / 256; k++) {
+          const int i = tid + 256 * k, q = i % (CH / 8), m = i / (CH / 8), n = m % kStates;
+          if (n >= ns || (PIECES % 256 && i >= PIECES)) continue;
+          load_row<T, 8>(piece(i, n0) - q * 8, c0 + q * 8, len, v);
+          put(i, v);
+        }
       }
       __syncthreads();
+      if (AHEAD && n0 + kStates < N)
+        fetch_bc(n0 + kStates, c0);
+      else if (AHEAD && c0 + CH < walk)
+        fetch_bc(0, c0 + CH);
       for (int n = 0; n < ns; n++) {
         const float2 Ah = ah[row * AH + n0 + n];
         float av[TI], bv[TI];
@@ -222,7 +274,11 @@ __global__ __launch_bounds__(256, 4) void scan_prompt(const sc_selective_scan a,
     if (!ENDS && live) {
       if (z) {
         float gate[TI];
-        load_row<T, TI>(z, t0, len, gate);
+        if (AHEAD && whole)
+#pragma unroll
+          for (int i = 0; i < TI; i++) gate[i] = (float)zr[i / 8 % AR][i % 8];
+        else
+          load_row<T, TI>(z, t0, len, gate);
 #pragma unroll
         for (int i = 0; i < TI; i++) y[i] *= silu(gate[i]);
       }
@@ -344,10 +400,21 @@ int launch_token(const sc_selective_scan& a, hipStream_t st) {
   return (int)hipGetLastError();
 }
 
-// How a prompt's scan is cut: positions per lane, and segments of the axis where there are few channels.
+// How a prompt's scan is cut.  Measured with 16 states, bf16, us, one sequence of D channels and L positions:
+//
+//   segments   D 512, L 8192   D 1024, L 1024   D 2048, L 8192   D 4096, L 2048
+//      1            256             34.5             268              70.8
+//      4            121             20.8             163              71.7
+//     16             50                              139
+//
+// so the axis is cut where fewer than 5/8 of the CUs have a workgroup, into 4 workgroups a CU or single
+// chunks; two segments cost what they save (two chunks: 18.4 and 19.5 us).  Reading ahead takes registers
+// that a fourth wavefront a SIMD could use: with up to 2 workgroups a CU it gains (D 4096, L 1024: 46.7 ->
+// 37.9 us), with 4 it loses (4 x 4096 x 2048: 166 -> 181 us).
 struct Plan {
-  int ti, chunks, segments;
-  int64_t groups;  // workgroups of a segment
+  int ti, chunks, segments;  // positions per lane
+  int64_t groups;            // workgroups of a segment
+  bool ahead;
 };
 
 Plan plan_of(const sc_selective_scan& a, int cus) {
@@ -356,35 +423,34 @@ Plan plan_of(const sc_selective_scan& a, int cus) {
   const int64_t share = a.D / a.G;
   p.groups = (int64_t)a.B * a.G * ((share + kRows - 1) / kRows);
   const int chunks = std::max(1, (a.L + 16 * p.ti - 1) / (16 * p.ti));
-  int64_t want = 1;
-  if (p.groups < cus) want = (4 * cus + p.groups - 1) / p.groups;
-  const int most = std::max(1, std::min(chunks / 2, 64));
-  int segments = (int)std::min<int64_t>(want, most);
-  if (p.ti < 16) segments = 1;
+  int segments = 1;
+  if (p.ti == 16 && 8 * p.groups <= 5 * cus) segments = (int)std::min<int64_t>(std::min(chunks, 64), (4 * cus + p.groups - 1) / p.groups);
+  if (segments < 3) segments = 1;
   p.chunks = (chunks + segments - 1) / segments;
   p.segments = (chunks + p.chunks - 1) / p.chunks;
+  p.ahead = p.ti == 16 && p.groups * p.segments <= 2 * cus;
   return p;
 }
 
-template <class T, int TI, bool ENDS>
+template <class T, int TI, bool ENDS, bool AHEAD>
 int launch_part(const sc_selective_scan& a, const Plan& p, const Split& sp, hipStream_t st) {
   const int lds = ((ENDS ? 1 : 2) * kStates * 16 * TI + (kRows + 1) * ah_pitch(a.N) * 2) * 4;
   const int64_t blocks = p.groups * (ENDS ? p.segments - 1 : p.segments);
-  hipLaunchKernelGGL((scan_prompt<T, TI, ENDS>), dim3((unsigned)blocks), dim3(256), lds, st, a, sp);
+  hipLaunchKernelGGL((scan_prompt<T, TI, ENDS, AHEAD>), dim3((unsigned)blocks), dim3(256), lds, st, a, sp);
   return (int)hipGetLastError();
 }
 
 template <class T>
 int launch_prompt(const sc_selective_scan& a, const Plan& p, hipStream_t st) {
   Split sp{p.segments, p.chunks, nullptr, nullptr};
-  if (p.ti == 4) return launch_part<T, 4, false>(a, p, sp, st);
-  if (p.ti == 8) return launch_part<T, 8, false>(a, p, sp, st);
+  if (p.ti == 4) return launch_part<T, 4, false, false>(a, p, sp, st);
+  if (p.ti == 8) return launch_part<T, 8, false, false>(a, p, sp, st);
   if (p.segments > 1) {
     sp.state = static_cast<float*>(a.workspace);
     sp.sum = sp.state + (int64_t)a.B * p.segments * a.D * a.N;
-    if (const int e = launch_part<T, 16, true>(a, p, sp, st)) return e;
+    if (const int e = p.ahead ? launch_part<T, 16, true, true>(a, p, sp, st) : launch_part<T, 16, true, false>(a, p, sp, st)) return e;
   }
-  return launch_part<T, 16, false>(a, p, sp, st);
+  return p.ahead ? launch_part<T, 16, false, true>(a, p, sp, st) : launch_part<T, 16, false, false>(a, p, sp, st);
 }
 
 template <class T>
