@@ -107,14 +107,23 @@ __global__ __launch_bounds__(64 * NW) void adapter_down(const sc_adapter a, floa
     for (int t = 0; t < RT; t++) wv[t] = *reinterpret_cast<const KVec*>(w[t] + c);
     product(xv, wv);
   }
-  if (blk < end) {  // the last channels: zeros in both operands
-    const int c = blk * 4 * X::K + part * X::K, nc = a.C - c;
+  if (blk < end) {  // the last channels; past them the last one is read, and zeros take its place
+    const int c = blk * 4 * X::K + part * X::K;
     Vec xv[X::K];
     KVec wv[RT];
 #pragma unroll
-    for (int i = 0; i < X::K; i++) xv[i] = load_some<T, X::V>(x + (c + i) * a.x_channel, i < nc ? X::V : 0);
+    for (int i = 0; i < X::K; i++) {
+      xv[i] = *reinterpret_cast<const Vec*>(x + min(c + i, a.C - 1) * a.x_channel);
 #pragma unroll
-    for (int t = 0; t < RT; t++) wv[t] = load_some<T, X::K>(w[t] + c, nc);
+      for (int t = 0; t < RT; t++) wv[t][i] = w[t][min(c + i, a.C - 1)];
+    }
+#pragma unroll
+    for (int i = 0; i < X::K; i++)
+      if (c + i >= a.C) {
+        xv[i] = Vec{};
+#pragma unroll
+        for (int t = 0; t < RT; t++) wv[t][i] = T(0.0f);
+      }
     product(xv, wv);
   }
   const float scale = a.scale ? a.scale[ad] : 1.0f;
@@ -140,19 +149,24 @@ __global__ __launch_bounds__(64 * NW) void adapter_down(const sc_adapter a, floa
   }
 }
 
-// The sum over the segments of 8 rows of low from r0 on, at one position; 0 past R (where the last row is
-// read instead: no branch stands between the loads).
-__device__ __forceinline__ void low_rows(const sc_adapter& a, const float* low, int segments, int b, int r0, int l,
-                                         float (&v)[8]) {
+// The sum over S segments of 8 rows of low from r0 on, at one position; 0 past R (where the last row is
+// read instead).  No branch stands between the 8 S loads: they come from L2 and are asked for at once.
+template <int S>
+__device__ __forceinline__ void low_rows(const sc_adapter& a, const float* low, int b, int r0, int l, float (&v)[8]) {
+  float u[S][8];
 #pragma unroll
-  for (int i = 0; i < 8; i++) v[i] = 0.0f;
-  for (int s = 0; s < segments; s++) {
+  for (int s = 0; s < S; s++) {
     const float* p = low + ((int64_t)s * a.B + b) * a.R * a.L + l;
 #pragma unroll
-    for (int i = 0; i < 8; i++) v[i] += p[(int64_t)min(r0 + i, a.R - 1) * a.L];
+    for (int i = 0; i < 8; i++) u[s][i] = p[(int64_t)min(r0 + i, a.R - 1) * a.L];
   }
 #pragma unroll
-  for (int i = 0; i < 8; i++) v[i] = r0 + i < a.R ? v[i] : 0.0f;
+  for (int i = 0; i < 8; i++) {
+    v[i] = u[0][i];
+#pragma unroll
+    for (int s = 1; s < S; s++) v[i] += u[s][i];
+    v[i] = r0 + i < a.R ? v[i] : 0.0f;
+  }
 }
 
 // out = base + up low for `mrows` output channels of one tile of positions.  low is held in LDS as the
@@ -160,9 +174,8 @@ __device__ __forceinline__ void low_rows(const sc_adapter& a, const float* low, 
 // one instruction (its 32 summed rows are 16 high parts and the same 16 low parts), so the
 // intermediate keeps 16 bits.  fp16's narrow exponent is met by a power of two per position.
 // The next 16 channels' base is on its way while these are computed and stored.
-template <class T>
-__global__ __launch_bounds__(256) void adapter_up(const sc_adapter a, const float* low, int segments, int ltiles,
-                                                  int mtiles, int mrows) {
+template <class T, int S>
+__global__ __launch_bounds__(256, 4) void adapter_up(const sc_adapter a, const float* low, int ltiles, int mtiles, int mrows) {
   typedef Tile<T> X;
   typedef typename X::Vec Vec;
   typedef typename X::KVec KVec;
@@ -175,6 +188,19 @@ __global__ __launch_bounds__(256) void adapter_up(const sc_adapter a, const floa
   const int m_begin = id % mtiles * mrows, b = id / mtiles;
   const int ad = adapter_of(a, b);
   const int R16 = (a.R + 15) / 16;
+  const int own = l0 + X::V * col, l = lane_start(l0, X::V, col, a.L);
+  const T* base = static_cast<const T*>(a.base);
+  if (base) base += b * a.base_batch + l;
+  const int m_end = min(a.M, m_begin + mrows);
+  Vec next[4] = {};
+  auto fetch = [&](int m0) {
+    if (base)
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        next[i] = *reinterpret_cast<const Vec*>(base + min(m0 + part * 4 + i, m_end - 1) * a.base_channel);
+  };
+  int m0 = m_begin + wave * 16;
+  if (m0 < m_end) fetch(m0);
   float back[X::V];  // 2^e of the lane's positions
 #pragma unroll
   for (int q = 0; q < X::V; q++) back[q] = 1.0f;
@@ -183,7 +209,7 @@ __global__ __launch_bounds__(256) void adapter_up(const sc_adapter a, const floa
       for (int i = tid; i < R16 * 2 * X::L; i += 256) {
         const int j = i % X::L, r0 = i / X::L * 8;
         float v[8];
-        low_rows(a, low, segments, b, r0, lane_start(l0, X::V, j / X::V, a.L) + j % X::V, v);
+        low_rows<S>(a, low, b, r0, lane_start(l0, X::V, j / X::V, a.L) + j % X::V, v);
 #pragma unroll
         for (int k = 0; k < 8; k++) lds[(r0 + k) * X::L + j] = v[k];
       }
@@ -197,7 +223,7 @@ __global__ __launch_bounds__(256) void adapter_up(const sc_adapter a, const floa
         float m = 0.0f;
         for (int k = 0; k < R16; k++) {
           float v[8];
-          low_rows(a, low, segments, b, k * 16 + half * 8, at, v);
+          low_rows<S>(a, low, b, k * 16 + half * 8, at, v);
 #pragma unroll
           for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(v[i]));
         }
@@ -217,7 +243,7 @@ __global__ __launch_bounds__(256) void adapter_up(const sc_adapter a, const floa
       KVec* op = reinterpret_cast<KVec*>(lds);  // [R16][8 tiles][64 lanes]
       for (int k = 0; k < R16; k++) {
         float v[8];
-        low_rows(a, low, segments, b, k * 16 + half * 8, at, v);
+        low_rows<S>(a, low, b, k * 16 + half * 8, at, v);
         KVec hi, lo;
 #pragma unroll
         for (int i = 0; i < 8; i++) {
@@ -234,20 +260,7 @@ __global__ __launch_bounds__(256) void adapter_up(const sc_adapter a, const floa
     }
   }
   const T* w = static_cast<const T*>(a.up) + (int64_t)max(ad, 0) * a.M * a.R;
-  const int own = l0 + X::V * col, l = lane_start(l0, X::V, col, a.L);
-  const T* base = static_cast<const T*>(a.base);
-  if (base) base += b * a.base_batch + l;
   T* out = static_cast<T*>(a.out) + b * a.out_batch + l;
-  const int m_end = min(a.M, m_begin + mrows);
-  Vec next[4] = {};
-  auto fetch = [&](int m0) {
-    if (base)
-#pragma unroll
-      for (int i = 0; i < 4; i++)
-        next[i] = *reinterpret_cast<const Vec*>(base + min(m0 + part * 4 + i, m_end - 1) * a.base_channel);
-  };
-  int m0 = m_begin + wave * 16;
-  if (m0 < m_end) fetch(m0);
   for (; m0 < m_end; m0 += 64) {
     Vec bv[4];
 #pragma unroll
@@ -402,11 +415,9 @@ Plan plan_of(const sc_adapter& a, int cus) {
   const int blocks = (a.C + (wide ? 16 : 32) - 1) / (wide ? 16 : 32);
   p.rpieces = (a.R + 63) / 64;
   const int nw = a.R <= 32 ? 8 : 4;
-  p.segments = (int)std::clamp<int64_t>((2 * cus + tiles * p.rpieces - 1) / (tiles * p.rpieces), 1,
-                                        std::max(1, std::min(blocks / nw, 4)));
-  // an empty last piece would leave its part of the workspace unwritten
-  const int per = (blocks + p.segments - 1) / p.segments;
-  p.segments = (blocks + per - 1) / per;
+  // 1, 2 or 4 pieces of C, so that every CU has a workgroup or two (an empty piece's sums are 0)
+  const int64_t want = 2 * cus / (tiles * p.rpieces);
+  p.segments = want >= 4 && blocks >= 4 * nw ? 4 : want >= 2 && blocks >= 2 * nw ? 2 : 1;
   p.mtiles = (int)std::clamp<int64_t>((4 * cus + tiles - 1) / tiles, 1, (a.M + 127) / 128);
   p.mrows = ((a.M + p.mtiles - 1) / p.mtiles + 63) / 64 * 64;
   p.mtiles = (a.M + p.mrows - 1) / p.mrows;
@@ -433,7 +444,12 @@ int launch_type(const sc_adapter& a, int cus, hipStream_t st) {
   if (const int e = (int)hipGetLastError()) return e;
   const int R16 = (a.R + 15) / 16;
   const int lds = sizeof(T) == 4 ? R16 * 16 * 64 * 4 : R16 * 8 * 64 * 16;
-  hipLaunchKernelGGL((adapter_up<T>), gu, dim3(256), lds, st, a, low, p.segments, p.ltiles, p.mtiles, p.mrows);
+  if (p.segments == 1)
+    hipLaunchKernelGGL((adapter_up<T, 1>), gu, dim3(256), lds, st, a, low, p.ltiles, p.mtiles, p.mrows);
+  else if (p.segments == 2)
+    hipLaunchKernelGGL((adapter_up<T, 2>), gu, dim3(256), lds, st, a, low, p.ltiles, p.mtiles, p.mrows);
+  else
+    hipLaunchKernelGGL((adapter_up<T, 4>), gu, dim3(256), lds, st, a, low, p.ltiles, p.mtiles, p.mrows);
   return (int)hipGetLastError();
 }
 
