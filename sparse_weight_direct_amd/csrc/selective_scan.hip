@@ -331,7 +331,8 @@ __device__ __forceinline__ void load_states(const T* p, int64_t stride, int n, f
   }
 }
 
-template <class T, int Q>
+// PLAIN: whole quads of states, and b and c contiguous over them: no branch between the loads.
+template <class T, int Q, bool PLAIN>
 __global__ __launch_bounds__(256) void scan_token(const sc_selective_scan a, int blocks) {
   constexpr int U = 4, CPP = 256 / Q;  // channels per thread; per workgroup and u
   typedef typename Pack<float, 4>::type F4;
@@ -340,33 +341,37 @@ __global__ __launch_bounds__(256) void scan_token(const sc_selective_scan a, int
   const int base = blockIdx.x % blocks * (U * CPP) + p, g = blockIdx.x / blocks % a.G, b = blockIdx.x / blocks / a.G;
   const int slot = slot_of(a.slots, a.num_slots, b);
   const bool on = slot >= 0 && length_of(a.lengths, 1, b) == 1;
-  const int own = min(base + k * CPP, share - 1), d = g * share + own;
-  const float x = (float)static_cast<const T*>(a.x)[b * a.x_batch + d * a.x_channel];
-  const float raw = (float)static_cast<const T*>(a.dt)[b * a.dt_batch + d * a.dt_channel] + (a.dt_bias ? a.dt_bias[d] : 0.0f);
-  const float gate = a.z ? (float)static_cast<const T*>(a.z)[b * a.z_batch + d * a.z_channel] : 0.0f;
-  const float skip = a.skip ? a.skip[d] : 0.0f;
   const T* bm = static_cast<const T*>(a.b) + b * a.b_batch + g * a.b_group;
   const T* cm = static_cast<const T*>(a.c) + b * a.c_batch + g * a.c_group;
   const int64_t c0 = (int64_t)(g * share) * a.N;
   const float* from = a.initial_state && slot >= 0 ? a.initial_state + slot * a.initial_stride + c0 : nullptr;
   float* to = a.final_state && slot >= 0 ? a.final_state + slot * a.final_stride + c0 : nullptr;
+  F4 h[U], A[U];
+  float bv[4], cv[4];
+  auto fetch = [&](int n0) {
+    const int ns = PLAIN ? 4 : a.N - n0;
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int64_t at = (int64_t)min(base + u * CPP, share - 1) * a.N + n0;
+      h[u] = from ? load_some<float, 4>(from + at, ns) : F4{0.0f, 0.0f, 0.0f, 0.0f};
+      A[u] = load_some<float, 4>(a.A + c0 + at, ns);
+    }
+    load_states(bm + n0 * a.b_state, PLAIN ? 1 : a.b_state, ns, bv);
+    load_states(cm + n0 * a.c_state, PLAIN ? 1 : a.c_state, ns, cv);
+  };
+  int n0 = q * 4;
+  if (n0 < a.N) fetch(n0);  // the states first: the longest way
+  const int own = min(base + k * CPP, share - 1), d = g * share + own;
+  const float x = (float)static_cast<const T*>(a.x)[b * a.x_batch + d * a.x_channel];
+  const float raw = (float)static_cast<const T*>(a.dt)[b * a.dt_batch + d * a.dt_channel] + (a.dt_bias ? a.dt_bias[d] : 0.0f);
+  const float gate = a.z ? (float)static_cast<const T*>(a.z)[b * a.z_batch + d * a.z_channel] : 0.0f;
+  const float skip = a.skip ? a.skip[d] : 0.0f;
   const float s_own = a.flags & SC_SEQ_SOFTPLUS ? softplus(raw) : raw, sx_own = s_own * x;
   const float s[U] = {dpp<0x00>(s_own), dpp<0x55>(s_own), dpp<0xaa>(s_own), dpp<0xff>(s_own)};
   const float sx[U] = {dpp<0x00>(sx_own), dpp<0x55>(sx_own), dpp<0xaa>(sx_own), dpp<0xff>(sx_own)};
   float y[U] = {};
-  for (int n0 = q * 4; n0 < a.N; n0 += 4 * Q) {
-    const int ns = a.N - n0;
-    F4 h[U], A[U];
-    float bv[4], cv[4];
-#pragma unroll
-    for (int u = 0; u < U; u++) {
-      const bool live = base + u * CPP < share;
-      const int64_t at = (int64_t)(live ? base + u * CPP : 0) * a.N + n0;
-      A[u] = load_some<float, 4>(a.A + c0 + at, ns);
-      h[u] = from ? load_some<float, 4>(from + at, ns) : F4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-    load_states(bm + n0 * a.b_state, a.b_state, ns, bv);
-    load_states(cm + n0 * a.c_state, a.c_state, ns, cv);
+  while (n0 < a.N) {
+    const int ns = PLAIN ? 4 : a.N - n0;
 #pragma unroll
     for (int u = 0; u < U; u++) {
       if (on)
@@ -377,6 +382,8 @@ __global__ __launch_bounds__(256) void scan_token(const sc_selective_scan a, int
         }
       if (to && base + u * CPP < share) store_some<float, 4>(to + (int64_t)(base + u * CPP) * a.N + n0, ns, h[u]);
     }
+    n0 += 4 * Q;
+    if (n0 < a.N) fetch(n0);
   }
   // the sum over the channel's lanes, in every lane: neighbours in a quad, then quads, then halves of a row
 #pragma unroll
@@ -396,7 +403,11 @@ __global__ __launch_bounds__(256) void scan_token(const sc_selective_scan a, int
 template <class T, int Q>
 int launch_token(const sc_selective_scan& a, hipStream_t st) {
   const int per = 4 * (256 / Q), blocks = (a.D / a.G + per - 1) / per;
-  hipLaunchKernelGGL((scan_token<T, Q>), dim3((unsigned)((int64_t)a.B * a.G * blocks)), dim3(256), 0, st, a, blocks);
+  const dim3 grid((unsigned)((int64_t)a.B * a.G * blocks));
+  if (a.N % 4 == 0 && a.b_state == 1 && a.c_state == 1)
+    hipLaunchKernelGGL((scan_token<T, Q, true>), grid, dim3(256), 0, st, a, blocks);
+  else
+    hipLaunchKernelGGL((scan_token<T, Q, false>), grid, dim3(256), 0, st, a, blocks);
   return (int)hipGetLastError();
 }
 
