@@ -37,7 +37,7 @@ struct View {
   bool empty() const { return !p || outer <= 0 || rows <= 0 || len <= 0; }
 };
 
-constexpr int64_t kMaxStride = 1LL << 40;  // with sizes below 2^31 no offset passes 2^63 bytes... checked by product
+constexpr int64_t kMaxStride = 1LL << 40;  // values; a tensor's whole span is held below 1e17 as well
 
 bool strides_ok(const View& v) {
   if (v.outer_stride < 0 || v.row_stride < 0 || v.outer_stride > kMaxStride || v.row_stride > kMaxStride) return false;
@@ -96,7 +96,8 @@ sc_status check_states(const void* first, int64_t first_stride, const void* last
   if (misaligned(first, es) || misaligned(last, es)) return fail(SC_EINVAL, "a state is misaligned");
   if (!slots && num_slots < B) return fail(SC_ESHAPE, "fewer state slots than sequences");
   for (int64_t stride : {first ? first_stride : per, last ? last_stride : per})
-    if (stride < per || stride > kMaxStride) return fail(SC_ESHAPE, "a state's slot stride is smaller than a state, or too large");
+    if (stride < per || stride > kMaxStride || (long double)num_slots * stride >= 1e17L)
+      return fail(SC_ESHAPE, "a state's slot stride is smaller than a state, or too large");
   if (first && last && !(first == last && first_stride == last_stride)) {
     const View f{first, 1, num_slots, per, 0, first_stride, es}, l{last, 1, num_slots, per, 0, last_stride, es};
     if (overlap(f, l)) return fail(SC_EINVAL, "initial_state and final_state overlap and are not the same");

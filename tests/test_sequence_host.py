@@ -57,7 +57,8 @@ CONV = [(dict(dtype=3), EINVAL), (dict(dtype=-1), EINVAL), (dict(flags=2), EINVA
         (dict(lengths=7 * A0 + 2), EINVAL), (dict(slots=7 * A0 + 1), EINVAL), (dict(initial=5 * A0 + 2), EINVAL),
         (dict(x_batch=-1), ESHAPE), (dict(x_channel=-16), ESHAPE), (dict(out_channel=1 << 41), ESHAPE),
         (dict(out_channel=15), EINVAL), (dict(out_batch=0), EINVAL), (dict(num_slots=1), ESHAPE), (dict(num_slots=-1), ESHAPE),
-        (dict(initial_stride=23), ESHAPE), (dict(final_stride=0), ESHAPE), (dict(final=5 * A0 + 4), EINVAL),
+        (dict(initial_stride=23), ESHAPE), (dict(num_slots=1 << 30, initial_stride=1 << 39), ESHAPE),
+        (dict(final_stride=0), ESHAPE), (dict(final=5 * A0 + 4), EINVAL),
         (dict(final=5 * A0, final_stride=48), EINVAL), (dict(out=A0), EINVAL), (dict(out=A0 + 64), EINVAL),
         (dict(out=5 * A0), EINVAL), (dict(out=6 * A0 - 4), EINVAL), (dict(final=A0), EINVAL), (dict(out=3 * A0), EINVAL),
         (dict(out=4 * A0 + 16), EINVAL), (dict(final=7 * A0 - 4), EINVAL)]
