@@ -317,6 +317,15 @@ def test_adapter_sizes(dtype, C, M, R, L):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("L", [256, 512, 1024, 1601])
+@pytest.mark.parametrize("R", [3, 16, 40])
+def test_adapter_long_rows(dtype, L, R):
+    """Four tiles of positions side by side, all of them there or the last set cut short."""
+    _check_adapter(_gen(L + R), dtype, 2, 70, 100, L, R, 3, index=[1, -1] if R == 3 else [2, 0])
+    _check_adapter(_gen(L), dtype, 1, 300, 65, L, R, 1, base="inplace", strided=True)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("L", [1, 37])
 def test_adapter_index_base_and_strides(dtype, L):
     g = _gen(L)
