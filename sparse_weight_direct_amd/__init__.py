@@ -9,8 +9,8 @@ The functions keep the C names:
     sparseconv_pack, sparseconv_forward, sparseconv_forward_workspace,
     sparseconv_workspace_size, sparseconv_query, sparseconv_export_packed,
     sparseconv_export_words, sparseconv_destroy, sparseconv_last_error
-plus the sequence operators (sequence.py) and ``Handle`` (owns a packed filter bank and destroys it when collected).  The dense
-direct baseline is a Handle packed with SC_PACK_ALL_TAPS (every filter tap stored).
+plus ``Handle`` (owns a packed filter bank and destroys it when collected) and the sequence
+operators (sequence.py; a pruned layer that uses them: ssm.py).  The dense direct baseline is a Handle packed with SC_PACK_ALL_TAPS (every filter tap stored).
 """
 from __future__ import annotations
 
