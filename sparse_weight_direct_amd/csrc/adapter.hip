@@ -418,7 +418,7 @@ struct Plan {
 Plan plan_of(const sc_adapter& a, int cus) {
   Plan p{};
   const bool wide = a.dtype == SC_F32;
-  p.token = a.L < 8;  // the tiles' lanes hold 8 positions
+  p.token = a.L < (wide ? 4 : 8);  // a tile's lane holds so many positions
   if (p.token) {
     p.mrows = kTokenRows * kToken;
     p.mtiles = (a.M + p.mrows - 1) / p.mrows;

@@ -191,14 +191,14 @@ sc_status sparseconv_selective_scan(const sc_selective_scan* a, void* hip_stream
     for (const void* p : {(const void*)a->A, (const void*)a->skip, (const void*)a->dt_bias, (const void*)a->lengths})
       if (misaligned(p, 4)) return fail(SC_EINVAL, "a pointer is not aligned to its type");
     const View out{a->out, a->B, a->D, a->L, a->out_batch, a->out_channel, es};
+    for (int64_t s : {a->b_state, a->c_state})
+      if (s < 0 || s > kMaxStride) return fail(SC_ESHAPE, "a stride is negative or too large");
     // of b and c the span alone: a (group, state) pair counts as one block of rows
     const View in[] = {{a->x, a->B, a->D, a->L, a->x_batch, a->x_channel, es},
                        {a->dt, a->B, a->D, a->L, a->dt_batch, a->dt_channel, es},
                        {a->z, a->B, a->D, a->L, a->z_batch, a->z_channel, es}};
     const View bc[] = {{a->b, a->B, a->G, (a->N - 1) * a->b_state + a->L, a->b_batch, a->b_group, es},
                        {a->c, a->B, a->G, (a->N - 1) * a->c_state + a->L, a->c_batch, a->c_group, es}};
-    for (int64_t s : {a->b_state, a->c_state})
-      if (s < 0 || s > kMaxStride) return fail(SC_ESHAPE, "a stride is negative or too large");
     for (const View& v : in)
       if (!strides_ok(v)) return fail(SC_ESHAPE, "a stride is negative or too large");
     for (const View& v : bc)

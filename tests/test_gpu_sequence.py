@@ -303,7 +303,7 @@ def _check_adapter(g, dtype, B, C, M, L, R, n, index=None, scale=True, base="giv
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("L", [1, 2, 3, 15, 16, 17, 31, 33, 64, 65, 127, 130, 200])
+@pytest.mark.parametrize("L", [1, 2, 3, 4, 5, 7, 8, 9, 15, 16, 17, 31, 33, 64, 65, 127, 130, 200])
 def test_adapter_lengths(dtype, L):
     _check_adapter(_gen(L), dtype, 3, 70, 90, L, 16, 4)
 
