@@ -325,9 +325,10 @@ __global__ __launch_bounds__(256, 4) void adapter_up(const sc_adapter a, const f
 // first kFront values of every row of up) is asked for before the first half begins.
 constexpr int kToken = 512;   // threads
 constexpr int kTokenRows = 2;   // output channels per thread
-constexpr int kFront = 16;
+constexpr int kFront = 16;  // (what follows takes them in 16s too)
 
-template <class T>
+// RW: rows of down per wavefront at a time.
+template <class T, int RW>
 __global__ __launch_bounds__(kToken) void adapter_token(const sc_adapter a, int mtiles, int mrows) {
   constexpr int V = 16 / sizeof(T), F = kFront / V;
   typedef typename Pack<T, V>::type Vec;
@@ -363,48 +364,70 @@ __global__ __launch_bounds__(kToken) void adapter_token(const sc_adapter a, int 
       for (int i = 0; i < V; i++) v[i] = x[(c + i) * a.x_channel];
       return v;
     };
-    // two rows at a time, four pieces of each in flight
-    for (int r = 2 * wave; r < a.R; r += 2 * (kToken / 64)) {
-      const T* w0 = w + (int64_t)r * a.C;
-      const T* w1 = w + (int64_t)min(r + 1, a.R - 1) * a.C;
-      float v0 = 0.0f, v1 = 0.0f;
+    // RW rows at a time, four pieces of each in flight
+    for (int r = RW * wave; r < a.R; r += RW * (kToken / 64)) {
+      const T* wr[RW];
+      float v[RW];
+#pragma unroll
+      for (int k = 0; k < RW; k++) wr[k] = w + (int64_t)min(r + k, a.R - 1) * a.C, v[k] = 0.0f;
       int c = lane * V;
 #pragma unroll 4
       for (; c + V <= a.C; c += 64 * V) {
-        const Vec xv = x_at(c), wv = *reinterpret_cast<const Vec*>(w0 + c), wu = *reinterpret_cast<const Vec*>(w1 + c);
+        const Vec xv = x_at(c);
+        Vec wv[RW];
 #pragma unroll
-        for (int i = 0; i < V; i++) v0 = fmaf((float)wv[i], (float)xv[i], v0), v1 = fmaf((float)wu[i], (float)xv[i], v1);
+        for (int k = 0; k < RW; k++) wv[k] = *reinterpret_cast<const Vec*>(wr[k] + c);
+#pragma unroll
+        for (int k = 0; k < RW; k++)
+#pragma unroll
+          for (int i = 0; i < V; i++) v[k] = fmaf((float)wv[k][i], (float)xv[i], v[k]);
       }
       for (int i = c; i < a.C && i < c + V; i++) {
         const float xv = (float)x[i * a.x_channel];
-        v0 = fmaf((float)w0[i], xv, v0), v1 = fmaf((float)w1[i], xv, v1);
+#pragma unroll
+        for (int k = 0; k < RW; k++) v[k] = fmaf((float)wr[k][i], xv, v[k]);
       }
 #pragma unroll
-      for (int m = 32; m; m >>= 1) v0 += __shfl_xor(v0, m), v1 += __shfl_xor(v1, m);
-      if (lane == 0) {
-        low[r] = scale * v0;
-        if (r + 1 < a.R) low[r + 1] = scale * v1;
-      }
+      for (int m = 32; m; m >>= 1)
+#pragma unroll
+        for (int k = 0; k < RW; k++) v[k] += __shfl_xor(v[k], m);
+      if (lane == 0)
+#pragma unroll
+        for (int k = 0; k < RW; k++)
+          if (r + k < a.R) low[r + k] = scale * v[k];
     }
   }
   __syncthreads();
+  float s[kTokenRows] = {};
+  if (ad >= 0) {
+    const T* um[kTokenRows];
+#pragma unroll
+    for (int k = 0; k < kTokenRows; k++) {
+      um[k] = up + (int64_t)min(mt * mrows + (int)threadIdx.x + k * kToken, a.M - 1) * a.R;
+#pragma unroll
+      for (int r = 0; r < kFront; r++)
+        if (r < a.R) s[k] = fmaf((float)front[k][r / V][r % V], low[r], s[k]);
+    }
+    int r = kFront;
+    for (; r + 16 <= a.R; r += 16) {  // sixteen more of every row at once
+      Vec wv[kTokenRows][F];
+#pragma unroll
+      for (int k = 0; k < kTokenRows; k++)
+#pragma unroll
+        for (int f = 0; f < F; f++) wv[k][f] = *reinterpret_cast<const Vec*>(um[k] + r + f * V);
+#pragma unroll
+      for (int k = 0; k < kTokenRows; k++)
+#pragma unroll
+        for (int i = 0; i < 16; i++) s[k] = fmaf((float)wv[k][i / V][i % V], low[r + i], s[k]);
+    }
+    for (; r < a.R; r++)
+#pragma unroll
+      for (int k = 0; k < kTokenRows; k++) s[k] = fmaf((float)um[k][r], low[r], s[k]);
+  }
 #pragma unroll
   for (int k = 0; k < kTokenRows; k++) {
     const int m = mt * mrows + threadIdx.x + k * kToken;
-    if (m >= a.M) continue;
-    float s = 0.0f;
-    if (ad >= 0) {
-#pragma unroll
-      for (int r = 0; r < kFront; r++)
-        if (r < a.R) s = fmaf((float)front[k][r / V][r % V], low[r], s);
-      for (int r = kFront; r < a.R; r += V) {
-        const Vec wv = load_some<T, V>(up + (int64_t)m * a.R + r, a.R - r);
-#pragma unroll
-        for (int i = 0; i < V; i++)
-          if (r + i < a.R) s = fmaf((float)wv[i], low[r + i], s);
-      }
-    }
-    static_cast<T*>(a.out)[b * a.out_batch + m * a.out_channel + l] = T((float)first[k] + s);
+    if (m < a.M) static_cast<T*>(a.out)[b * a.out_batch + m * a.out_channel + l] = T((float)first[k] + s[k]);
   }
 }
 
@@ -433,8 +456,10 @@ Plan plan_of(const sc_adapter& a, int cus) {
   const int64_t want = 2 * cus / (tiles * p.rpieces);
   p.segments = want >= 4 && blocks >= 4 * nw ? 4 : want >= 2 && blocks >= 2 * nw ? 2 : 1;
   // Four wavefronts side by side read and write 1 KB of a row together instead of 256 bytes (fp32,
-  // 8 x 2048 -> 4096 x 1024: 78 -> 73 us), where that leaves few of them idle and LDS holds four tiles.
-  p.wide = a.R <= 16 && (p.ltiles % 4 == 0 || p.ltiles >= 12);
+  // 8 x 2048 -> 4096 x 1024: 78 -> 73 us), where that leaves few of them idle, LDS holds four tiles and
+  // there is a workgroup for every CU and more (bf16, 8 x 2048 -> 2048 x 512, 128 of them: 24.9 us against 16.4).
+  p.wide = a.R <= 16 && (p.ltiles % 4 == 0 || p.ltiles >= 12) &&
+           (int64_t)a.B * ((p.ltiles + 3) / 4) * ((a.M + 127) / 128) >= 3 * cus;
   const int64_t sets = (int64_t)a.B * (p.wide ? (p.ltiles + 3) / 4 : p.ltiles);
   p.mtiles = (int)std::clamp<int64_t>((4 * cus + sets - 1) / sets, 1, (a.M + 127) / 128);
   p.mrows = ((a.M + p.mtiles - 1) / p.mtiles + 63) / 64 * 64;
@@ -458,7 +483,10 @@ int launch_type(const sc_adapter& a, int cus, hipStream_t st) {
   const Plan p = plan_of(a, cus);
   if (p.token) {
     const int64_t n = (int64_t)a.B * a.L * p.mtiles;
-    hipLaunchKernelGGL((adapter_token<T>), dim3((unsigned)n), dim3(kToken), 0, st, a, p.mtiles, p.mrows);
+    if (a.R <= 16)
+      hipLaunchKernelGGL((adapter_token<T, 2>), dim3((unsigned)n), dim3(kToken), 0, st, a, p.mtiles, p.mrows);
+    else
+      hipLaunchKernelGGL((adapter_token<T, 4>), dim3((unsigned)n), dim3(kToken), 0, st, a, p.mtiles, p.mrows);
     return (int)hipGetLastError();
   }
   float* low = static_cast<float*>(a.workspace);
