@@ -433,6 +433,18 @@ int launch_token(const sc_selective_scan& a, hipStream_t st) {
 // chunks; two segments cost what they save (two chunks: 18.4 and 19.5 us).  Reading ahead takes registers
 // that a fourth wavefront a SIMD could use: with up to 2 workgroups a CU it gains (D 4096, L 1024: 46.7 ->
 // 37.9 us), with 4 it loses (4 x 4096 x 2048: 166 -> 181 us).
+//
+// Positions a lane (a chunk is 16 lanes of them); a chunk that is not whole is padded and takes the guarded loads:
+//
+//   B x D       a lane   L 160   L 256   L 300   L 384   L 520
+//   8 x 4096      16      46.4    43.4    87.1    84.5   125.7
+//                  8      45.2    43.8    67.8    65.2   107.5
+//   1 x 4096      16      14.6    11.1    25.5    23.7    32.8
+//                  8      13.7    12.6    20.8    19.7    32.1
+//   1 x 1024      16      14.3    10.8    24.6    22.0    24.3
+//                  8      13.4    12.4    19.4    17.2    27.9
+//
+// so eight up to 384 positions unless they fill a chunk of sixteens; above, the two change places with every chunk.
 struct Plan {
   int ti, chunks, segments;  // positions per lane
   int64_t groups;            // workgroups of a segment
@@ -441,7 +453,8 @@ struct Plan {
 
 Plan plan_of(const sc_selective_scan& a, int cus) {
   Plan p;
-  p.ti = a.L <= 64 ? 4 : a.L <= 128 || a.N > 239 ? 8 : 16;  // beyond 239 states 16 would pass 64 KB of LDS
+  const bool eight = a.L <= 384 && a.L != 256;
+  p.ti = a.L <= 64 ? 4 : eight || a.N > 239 ? 8 : 16;  // beyond 239 states 16 would pass 64 KB of LDS
   const int64_t share = a.D / a.G;
   p.groups = (int64_t)a.B * a.G * ((share + kRows - 1) / kRows);
   const int chunks = std::max(1, (a.L + 16 * p.ti - 1) / (16 * p.ti));

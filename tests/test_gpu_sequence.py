@@ -206,6 +206,13 @@ def test_scan_of_few_rows_over_a_long_axis(L):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("L", [192, 320, 383, 384, 385, 512, 513])
+def test_scan_lengths_around_whole_chunks(dtype, L):
+    _check_scan(_gen(L), dtype, 2, 19, L, 16, state="both")
+    _check_scan(_gen(L), dtype, 3, 18, L, 24, 2, lengths=[L, 129, 0], state="inplace", strided=True)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("N,G,D,L", [(24, 2, 40, 1100), (5, 1, 17, 769), (64, 1, 16, 1500), (239, 1, 4, 800), (256, 1, 4, 800)])
 def test_scan_in_segments(dtype, N, G, D, L):
     _check_scan(_gen(N), dtype, 2, D, L, N, G, state="both", z=N != 5)
