@@ -389,7 +389,8 @@ __global__ __launch_bounds__(256) void scan_token(const sc_selective_scan a, int
 #pragma unroll
         for (int j = 0; j < 4; j++) {
           h[u][j] = fmaf(exp2_fast(s[u] * (A[u][j] * kLog2e)), h[u][j], sx[u] * bv[j]);
-          y[u] = fmaf(cv[j], h[u][j], y[u]);
+          // states past N are not added: 0 times an infinite step or input is no 0
+          if (PLAIN || j < ns) y[u] = fmaf(cv[j], h[u][j], y[u]);
         }
       if (to && base + u * CPP < share) store_some<float, 4>(to + (int64_t)(base + u * CPP) * a.N + n0, ns, h[u]);
     }
