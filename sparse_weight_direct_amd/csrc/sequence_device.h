@@ -48,11 +48,13 @@ __device__ __forceinline__ float silu(float v) {
 // log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|), to 4.3 x 2^-24 of every result (measured over
 // -40..25): the small ones count (time steps of 1e-3).  With u = 1 + e rounded, e - (u - 1) is what the
 // rounding lost, exactly, and log1p(e) = log(u) + that / u, where / u changes less than a rounding.
-// exp2's argument carries its rounding error along.  13 instructions; the math library's log1p alone is
+// exp2's argument carries its rounding error along; |v| is bounded for that (e is 0 from 88 on), or the
+// product would be infinite at the ends of the range and the error no number: softplus(-inf) is 0 and
+// softplus(inf) is inf.  The maximum keeps a NaN.  14 instructions; the math library's log1p alone is
 // 110, which was half of the whole scan's time (scan_prompt's shape: 259 us, and 175 with a polynomial of
 // 18 in its place).
 __device__ __forceinline__ float softplus(float v) {
-  const float m = -fabsf(v), p = m * kLog2e;
+  const float m = __builtin_elementwise_maximum(-fabsf(v), -126.0f), p = m * kLog2e;
   const float rest = fmaf(m, 1.92596299e-8f, fmaf(m, kLog2e, -p));  // log2(e) - kLog2e = 1.926e-8
   float e = exp2_fast(p);
   e = fmaf(e * 0.69314718f, rest, e);

@@ -33,3 +33,114 @@ def test_scan_step_infinite_input_at_any_state_size(dtype, N):
     assert torch.equal(state[0, 4], b[0, 0].float().sign() * INF) and torch.equal(state[2, 20], b[2, 0].float().sign() * -INF)
     out[0, 4], out[2, 20] = 0.0, 0.0
     assert torch.isfinite(out).all()
+
+
+# ---- steps at the ends of their type
+
+
+def _scan(s, **kw):
+    return sc.selective_scan(s["x"], s["dt"], s["A"], s["B"], s["C"], D=s["D"], z=s["z"], dt_bias=s["dt_bias"], **kw)
+
+
+def _scan_ref(s, first):
+    return ref.selective_scan(s["x"], s["dt"], s["A"], s["B"], s["C"], s["D"], s["z"], s["dt_bias"], True, None, None, first,
+                              first)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("low", ["-inf", "lowest"])
+@pytest.mark.parametrize("L", [1, 2, 100, 300, 520, 1100])
+def test_scan_steps_switched_off(dtype, low, L):
+    """softplus of -inf, and of the type's lowest value, is 0: the position adds nothing and the state stays.
+    The oracle takes -200 in their place, whose step is 1e-87."""
+    g = _gen(L)
+    s = _scan_inputs(g, dtype, 2, 18, L, 16, 2)
+    off = torch.rand(2, 18, L, generator=g, device="cuda") < 0.4
+    off[:, 3], off[0, :, 0] = True, True  # a whole channel, and the first position of a sequence
+    value = -INF if low == "-inf" else torch.finfo(dtype).min
+    first = _randn(g, 2, 18, 16)
+    s["dt"] = torch.where(off, -200.0, s["dt"].float()).to(dtype)
+    want, bound, P, PB = _scan_ref(s, first)
+    s["dt"] = torch.where(off, value, s["dt"].float()).to(dtype)
+    state = first.clone()
+    out = _scan(s, initial_state=state, final_state=state)
+    ref.assert_within(out, want, bound, "scan")
+    ref.assert_within(state, P, PB, "scan state")
+    assert torch.equal(state[:, 3], first[:, 3])
+    if L == 1:
+        state = first.clone()
+        one = {k: s[k][..., 0] for k in ("x", "dt", "z", "B", "C")}
+        out = sc.selective_scan_step(one["x"], state, one["dt"], s["A"], one["B"], one["C"], D=s["D"], z=one["z"],
+                                     dt_bias=s["dt_bias"])
+        ref.assert_within(out[:, :, None], want, bound, "scan step")
+        ref.assert_within(state, P, PB, "scan step state")
+
+
+def test_scan_bias_switches_channels_off():
+    """-inf (and -3e38) in dt_bias: no step of the channel, ever."""
+    g = _gen(31)
+    for L in (1, 40, 600):
+        s = _scan_inputs(g, torch.float32, 2, 24, L, 16, 1)
+        first = _randn(g, 2, 24, 16)
+        s["dt_bias"][5], s["dt_bias"][17] = -200.0, -200.0
+        want, bound, P, PB = _scan_ref(s, first)
+        s["dt_bias"][5], s["dt_bias"][17] = -INF, -3e38
+        state = first.clone()
+        ref.assert_within(_scan(s, initial_state=state, final_state=state), want, bound, "scan")
+        ref.assert_within(state, P, PB, "scan state")
+        assert torch.equal(state[:, [5, 17]], first[:, [5, 17]])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("L,at", [(1, 0), (40, 25), (300, 299), (600, 310), (1100, 1099), (1100, 700)])
+def test_scan_largest_steps(dtype, L, at):
+    """The type's largest value is its own softplus, and exp(s A) is 0: the state is s b x, whatever came
+    before.  Four fp32 roundings make it (softplus's, dt's and dt_bias's sum, s x, its product with b; softplus is off by
+    4.3 units), so the state is within 8 units of 2^-24, the sum over N states within N + 12 of its
+    magnitudes, and silu as in the oracle."""
+    g = _gen(at)
+    N = 16
+    s = _scan_inputs(g, dtype, 2, 18, L, N, 1)
+    most = torch.finfo(dtype).max
+    tiny = 2.0 ** -125 if dtype != torch.float16 else 2.0 ** -14
+    s["dt"][:, :, at] = most
+    s["x"][:, :, at] = (s["x"][:, :, at].float().sign() * tiny).to(dtype)
+    s["x"][:, :, at] = torch.where(s["x"][:, :, at] == 0, tiny, s["x"][:, :, at].float()).to(dtype)
+    state = _randn(g, 2, 18, N)
+    out = _scan(s, initial_state=state, final_state=state)
+    X, T, b, c, Z = (ref.f64(s[k])[..., at] for k in ("x", "dt", "B", "C", "z"))
+    h = ((T + ref.f64(s["dt_bias"])) * X)[:, :, None] * b
+    y = (h * c).sum(2) + ref.f64(s["D"]) * X
+    mag = np.abs(h * c).sum(2) + np.abs(ref.f64(s["D"]) * X)
+    gate, ge = ref.silu_of(Z, 0.0)
+    err = (N + 12) * ref.U * mag
+    want, err = y * gate, np.abs(gate) * err + (np.abs(y) + err) * ge + ref.U * np.abs(y * gate)
+    ref.assert_within(out[:, :, at], want, ref.rounded(want, err, dtype), "output")
+    if at == L - 1:
+        ref.assert_within(state, h, 8 * ref.U * np.abs(h) + 2.0 ** -126, "state")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("L,at", [(1, 0), (40, 25), (600, 310), (1100, 700)])
+@pytest.mark.parametrize("value", [INF, NAN])
+def test_scan_steps_not_finite(dtype, L, at, value):
+    """An infinite step makes the state b x infinite with that sign, a NaN makes it NaN; what came before
+    and the other channels are as without it."""
+    g = _gen(at)
+    s = _scan_inputs(g, dtype, 2, 20, L, 1, 1, z=False)
+    first = _randn(g, 2, 20, 1)
+    states = [first.clone(), first.clone()]
+    clean = _scan(s, initial_state=states[0], final_state=states[0])
+    s["dt"][1, 7, at] = value
+    out = _scan(s, initial_state=states[1], final_state=states[1])
+    keep = torch.ones(2, 20, L, dtype=torch.bool, device="cuda")
+    keep[1, 7, at:] = False
+    assert torch.equal(out[keep], clean[keep])
+    assert not torch.isfinite(out[1, 7, at:]).any() and not torch.isfinite(states[1][1, 7]).any()
+    here = out[1, 7, at].item()
+    if value == INF:
+        assert here == INF * float(s["x"][1, 7, at].sign() * s["B"][1, 0, 0, at].sign() * s["C"][1, 0, 0, at].sign())
+    else:
+        assert np.isnan(here) and torch.isnan(out[1, 7, at:]).all() and torch.isnan(states[1][1, 7]).all()
+    states[0][1, 7] = states[1][1, 7] = 0.0
+    assert torch.equal(*states)
