@@ -211,7 +211,7 @@ __global__ __launch_bounds__(256, AHEAD ? 2 : 4) void scan_prompt(const sc_selec
 #pragma unroll
     for (int i = 0; i < TI; i++) {
       sx[i] = s[i] * y[i];
-      y[i] *= skip;
+      y[i] = a.skip ? y[i] * skip : 0.0f;  // without skip no term at all: 0 times an infinite x is no 0
       sum += s[i];
     }
     total += sum;
@@ -406,7 +406,8 @@ __global__ __launch_bounds__(256) void scan_token(const sc_selective_scan a, int
     if (Q >= 16) y[u] += dpp<0x140>(y[u]);
   }
   if (q < U && base + k * CPP < share) {
-    float o = fmaf(skip, x, k == 0 ? y[0] : k == 1 ? y[1] : k == 2 ? y[2] : y[3]);
+    const float sum = k == 0 ? y[0] : k == 1 ? y[1] : k == 2 ? y[2] : y[3];
+    float o = a.skip ? fmaf(skip, x, sum) : sum;
     if (a.z) o *= silu(gate);
     static_cast<T*>(a.out)[b * a.out_batch + d * a.out_channel] = T(on ? o : 0.0f);
   }

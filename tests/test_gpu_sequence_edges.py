@@ -144,3 +144,17 @@ def test_scan_steps_not_finite(dtype, L, at, value):
         assert np.isnan(here) and torch.isnan(out[1, 7, at:]).all() and torch.isnan(states[1][1, 7]).all()
     states[0][1, 7] = states[1][1, 7] = 0.0
     assert torch.equal(*states)
+
+
+# ---- an infinite input where there is no skip
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("L,at", [(1, 0), (40, 39), (520, 519), (600, 300)])
+def test_scan_infinite_input_without_skip(dtype, L, at):
+    """Without D there is no term in x itself: the output is c b s x, infinite, and not 0 times infinity."""
+    g = _gen(at + 1)
+    s = _scan_inputs(g, dtype, 2, 20, L, 1, 1, z=False, skip=False)
+    s["x"][0, 4, at] = -INF
+    want = -INF * float(s["B"][0, 0, 0, at].sign() * s["C"][0, 0, 0, at].sign())
+    assert _scan(s)[0, 4, at].item() == want
