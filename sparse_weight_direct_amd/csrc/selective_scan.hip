@@ -211,9 +211,12 @@ __global__ __launch_bounds__(256, AHEAD ? 2 : 4) void scan_prompt(const sc_selec
 #pragma unroll
     for (int i = 0; i < TI; i++) {
       sx[i] = s[i] * y[i];
-      y[i] = a.skip ? y[i] * skip : 0.0f;  // without skip no term at all: 0 times an infinite x is no 0
+      y[i] *= skip;
       sum += s[i];
     }
+    if (!a.skip)  // no term in x at all: 0 times an infinite x is no 0
+#pragma unroll
+      for (int i = 0; i < TI; i++) y[i] = 0.0f;
     total += sum;
     for (int n0 = 0; n0 < N; n0 += kStates) {
       const int ns = min(kStates, N - n0);
@@ -376,7 +379,7 @@ __global__ __launch_bounds__(256) void scan_token(const sc_selective_scan a, int
   const float x = (float)static_cast<const T*>(a.x)[b * a.x_batch + d * a.x_channel];
   const float raw = (float)static_cast<const T*>(a.dt)[b * a.dt_batch + d * a.dt_channel] + (a.dt_bias ? a.dt_bias[d] : 0.0f);
   const float gate = a.z ? (float)static_cast<const T*>(a.z)[b * a.z_batch + d * a.z_channel] : 0.0f;
-  const float skip = a.skip ? a.skip[d] : 0.0f;
+  const float skip = a.skip ? a.skip[d] : 0.0f, x_skip = a.skip ? x : 0.0f;  // x may be infinite
   const float s_own = a.flags & SC_SEQ_SOFTPLUS ? softplus(raw) : raw, sx_own = s_own * x;
   const float s[U] = {dpp<0x00>(s_own), dpp<0x55>(s_own), dpp<0xaa>(s_own), dpp<0xff>(s_own)};
   const float sx[U] = {dpp<0x00>(sx_own), dpp<0x55>(sx_own), dpp<0xaa>(sx_own), dpp<0xff>(sx_own)};
@@ -406,8 +409,7 @@ __global__ __launch_bounds__(256) void scan_token(const sc_selective_scan a, int
     if (Q >= 16) y[u] += dpp<0x140>(y[u]);
   }
   if (q < U && base + k * CPP < share) {
-    const float sum = k == 0 ? y[0] : k == 1 ? y[1] : k == 2 ? y[2] : y[3];
-    float o = a.skip ? fmaf(skip, x, sum) : sum;
+    float o = fmaf(skip, x_skip, k == 0 ? y[0] : k == 1 ? y[1] : k == 2 ? y[2] : y[3]);
     if (a.z) o *= silu(gate);
     static_cast<T*>(a.out)[b * a.out_batch + d * a.out_channel] = T(on ? o : 0.0f);
   }
