@@ -178,7 +178,11 @@ __device__ __forceinline__ void low_rows(const sc_adapter& a, const float* low, 
 // out = base + up low for `mrows` output channels of one tile of positions.  low is held in LDS as the
 // matrix cores take it: fp32 as it is; for 16-bit types as the sum of two 16-bit values, which share
 // one instruction (its 32 summed rows are 16 high parts and the same 16 low parts), so the
-// intermediate keeps 16 bits.  fp16's narrow exponent is met by a power of two per position.
+// intermediate keeps 16 bits (bf16) or 22 (fp16): a choice, by which an output is off by up to 2^-16 (2^-22)
+// of its terms' magnitudes before its own rounding, which is off by 2^-8 (2^-11) of their sum.  fp16's
+// narrow exponent is met by a power of two per position.  Where something infinite meets the parts (a
+// weight, whose product with a part that is 0 or has the other sign is NaN, or a value that only fp32
+// holds) they are no longer the value: sums that are not finite are made again from the fp32 values.
 // The next 16 channels' base is on its way while these are computed and stored.
 template <class T, int S, int WL>
 __global__ __launch_bounds__(256, 4) void adapter_up(const sc_adapter a, const float* low, int ltiles, int mtiles, int mrows) {
@@ -297,6 +301,32 @@ __global__ __launch_bounds__(256, 4) void adapter_up(const sc_adapter a, const f
           const KVec* op = reinterpret_cast<const KVec*>(operand) + k * 8 * 64 + lane;
 #pragma unroll
           for (int q = 0; q < X::V; q++) acc[q] = mfma(wv, op[q * 64], acc[q]);
+        }
+      }
+      if constexpr (!kWide) {
+        float none = 0.0f;
+#pragma unroll
+        for (int q = 0; q < X::V; q++)
+#pragma unroll
+          for (int i = 0; i < 4; i++) none = fmaf(acc[q][i], 0.0f, none);
+        if (__builtin_expect(__any(none != 0.0f), false)) {
+          int at = l, k = part;
+          asm volatile("" : "+v"(at), "+v"(k));  // keeps what follows from them out of the loop's registers
+#pragma unroll
+          for (int q = 0; q < X::V; q++) {
+            F4 again = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+            for (int r0 = 0; r0 < a.R; r0 += 4) {
+              const int r = r0 + k;
+              float v = 0.0f;
+              if (r < a.R)
+#pragma unroll 1
+                for (int s = 0; s < S; s++) v += low[(((int64_t)s * a.B + b) * a.R + r) * a.L + at + q];
+              again = __builtin_amdgcn_mfma_f32_16x16x4f32(r < a.R ? (float)wm[r] : 0.0f, v, again, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) acc[q][i] = __builtin_isfinite(acc[q][i]) ? acc[q][i] : again[i] / back[q];
+          }
         }
       }
     }

@@ -158,3 +158,61 @@ def test_scan_infinite_input_without_skip(dtype, L, at):
     s["x"][0, 4, at] = -INF
     want = -INF * float(s["B"][0, 0, 0, at].sign() * s["C"][0, 0, 0, at].sign())
     assert _scan(s)[0, 4, at].item() == want
+
+
+# ---- adapters: values that leave a 16-bit type
+
+
+def _adapter64(x, down, up, index, scale, base):
+    X, d, u, s, v = ref.f64(x), ref.f64(down), ref.f64(up), ref.f64(scale), ref.f64(base).copy()
+    with np.errstate(invalid="ignore"):
+        for b, r in enumerate(index):
+            low = s[r] * (d[r] @ X[b])
+            v[b] += (u[r][:, :, None] * low[None]).sum(1)
+    return v
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("L", [1, 7, 8, 40, 260])
+@pytest.mark.parametrize("R", [1, 5, 16, 24])
+def test_adapter_infinite_weights(dtype, L, R):
+    """An infinity in up gives one where the R values are not 0, or NaN where two of opposite sign meet; the
+    rows without one are what they were.  The R values lie in 0.5 .. 1.5 times scale, C of equal sign summed."""
+    g = _gen(L + R)
+    B, C, M, n = 2, 12, 37, 3
+    x = (torch.rand(B, C, L, generator=g, device="cuda") + 0.5).to(dtype)
+    down = (torch.rand(n, R, C, generator=g, device="cuda") + 0.5).to(dtype)
+    up, base = _randn(g, n, M, R, dtype=dtype), _randn(g, B, M, L, dtype=dtype)
+    scale = torch.tensor([1.0, -0.75, 0.5], device="cuda")
+    index = [1, 2]
+    want, bound = ref.adapter(x, down, up, index, scale, base)
+    for r in range(n):
+        up[r, 3, 0], up[r, 20, R - 1], up[r, 36, R // 2] = INF, -INF, INF
+        if R > 1:
+            up[r, 11, 0], up[r, 11, 1] = INF, -INF
+    exact = _adapter64(x, down, up, index, scale, base)
+    out = sc.adapter_apply(x, down, up, _ints(index), scale=scale, base=base)
+    got, finite = ref.f64(out), np.isfinite(exact)
+    assert (~finite).any() and (got[~finite].astype(np.float32).view(np.uint32) == exact[~finite].astype(np.float32).view(np.uint32))[
+        ~np.isnan(exact[~finite])].all()
+    assert np.isnan(got[np.isnan(exact)]).all()
+    keep = np.ones(M, bool)
+    keep[[3, 11, 20, 36]] = False
+    ref.assert_within(out[:, torch.tensor(keep, device="cuda")], want[:, keep], bound[:, keep], "adapter")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("R", [1, 16, 40])
+def test_adapter_large_intermediate(dtype, R):
+    """R values between a 16-bit type's largest and fp32's, met by weights that bring the result back."""
+    g = _gen(R)
+    B, C, M, n = 2, 2, 21, 1
+    for L in (3, 9, 50, 300):
+        big = torch.finfo(dtype).max if dtype != torch.float32 else 2.0 ** 127 * 1.9
+        x = torch.zeros(B, C, L, device="cuda")
+        x[:, 0], x[:, 1] = big, big * 2.0 ** -8 if dtype != torch.float16 else big  # fp16: past its range; the others: near fp32's
+        down = torch.ones(n, R, C, device="cuda", dtype=dtype)
+        up = (_randn(g, n, M, R) * (2.0 ** -12 if dtype == torch.float16 else 2.0 ** -100)).to(dtype)
+        x, base = x.to(dtype), torch.zeros(B, M, L, device="cuda", dtype=dtype)
+        want, bound = ref.adapter(x, down, up, [0, 0], None, base)
+        ref.assert_within(sc.adapter_apply(x, down, up, _ints([0, 0]), base=base), want, bound, f"L {L}")
