@@ -73,9 +73,10 @@ struct Call {
     *stride = shape[0] > 1 ? t.stride(0) : D * per;
     return shape[0];
   }
-  // both pools; returns the number of slots (B where there is no pool)
-  int32_t pools(PyObject* first, PyObject* last, at::ScalarType ty, int64_t B, int64_t D, int64_t per, const void** fp, void** lp,
-                int64_t* fs, int64_t* ls) const {
+  // both pools; returns the number of slots (B where there is no pool).  A pool of none has no address, so
+  // the library could not tell it from no pool at all.
+  int32_t pools(PyObject* first, PyObject* last, PyObject* slots, at::ScalarType ty, int64_t B, int64_t D, int64_t per,
+                const void** fp, void** lp, int64_t* fs, int64_t* ls) const {
     int64_t n = B;
     void* p = nullptr;
     *fp = *lp = nullptr;
@@ -92,6 +93,7 @@ struct Call {
       if (first != Py_None && m != n) refuse("initial_state and final_state have different numbers of slots");
       n = m;
     }
+    if (n == 0 && B > 0 && per > 0 && slots == Py_None) refuse("a pool of states without slots: fewer than sequences");
     return size(n);
   }
   static int32_t size(int64_t v) {
@@ -136,7 +138,7 @@ PyObject* causal_conv(PyObject* const* v, Py_ssize_t n) {
   a.flags = PyObject_IsTrue(v[3]) ? SC_SEQ_SILU : 0;
   a.lengths = c.dense<int32_t>(v[4], "lengths", at::kInt, {B});
   a.slots = c.dense<int32_t>(v[5], "slots", at::kInt, {B});
-  a.num_slots = c.pools(v[6], v[7], c.type, B, D, K - 1, &a.initial_state, &a.final_state, &a.initial_stride, &a.final_stride);
+  a.num_slots = c.pools(v[6], v[7], v[5], c.type, B, D, K - 1, &a.initial_state, &a.final_state, &a.initial_stride, &a.final_stride);
   const Tensor out = c.output(v[8], x.sizes(), axes == 3);
   a.x = x.data_ptr(), a.out = out.data_ptr();
   a.x_batch = x.stride(0), a.x_channel = x.stride(1), a.out_batch = out.stride(0), a.out_channel = out.stride(1);
@@ -176,7 +178,7 @@ PyObject* selective_scan(PyObject* const* v, Py_ssize_t n) {
   a.slots = c.dense<int32_t>(v[10], "slots", at::kInt, {B});
   const void* first;
   void* last;
-  a.num_slots = c.pools(v[11], v[12], at::kFloat, B, D, N, &first, &last, &a.initial_stride, &a.final_stride);
+  a.num_slots = c.pools(v[11], v[12], v[10], at::kFloat, B, D, N, &first, &last, &a.initial_stride, &a.final_stride);
   a.initial_state = static_cast<const float*>(first), a.final_state = static_cast<float*>(last);
   const Tensor out = c.output(v[13], x.sizes(), prompt);
   a.x = x.data_ptr(), a.dt = dt.data_ptr(), a.b = Bm.data_ptr(), a.c = Cm.data_ptr(), a.out = out.data_ptr();

@@ -216,3 +216,22 @@ def test_adapter_large_intermediate(dtype, R):
         x, base = x.to(dtype), torch.zeros(B, M, L, device="cuda", dtype=dtype)
         want, bound = ref.adapter(x, down, up, [0, 0], None, base)
         ref.assert_within(sc.adapter_apply(x, down, up, _ints([0, 0]), base=base), want, bound, f"L {L}")
+
+
+# ---- state pools without slots
+
+
+def test_empty_pools_are_refused():
+    """A pool of no slots holds no sequence's state; with slots that all point outside it every row is idle."""
+    x, w = torch.ones(2, 8, 16, device="cuda"), torch.ones(8, 4, device="cuda")
+    A, bc = -torch.ones(8, 4, device="cuda"), torch.ones(2, 1, 4, 16, device="cuda")
+    cs, hs = torch.empty(0, 8, 3, device="cuda"), torch.empty(0, 8, 4, device="cuda")
+    for f in (lambda: sc.causal_conv(x, w, initial_state=cs), lambda: sc.causal_conv(x, w, final_state=cs),
+              lambda: sc.causal_conv_step(x[..., 0], cs, w), lambda: sc.selective_scan(x, x, A, bc, bc, initial_state=hs),
+              lambda: sc.selective_scan(x, x, A, bc, bc, final_state=hs),
+              lambda: sc.selective_scan_step(x[..., 0], hs, x[..., 0], A, bc[..., 0], bc[..., 0])):
+        with pytest.raises((ValueError, sc.SparseConvError)):
+            f()
+    idle = _ints([0, 5])
+    assert not sc.causal_conv(x, w, slots=idle, initial_state=cs, final_state=cs).any()
+    assert not sc.selective_scan_step(x[..., 0], hs, x[..., 0], A, bc[..., 0], bc[..., 0], slots=idle).any()
