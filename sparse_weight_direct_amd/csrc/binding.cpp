@@ -5,11 +5,15 @@
 //
 // Each function takes every argument by position (None where one is left out) and the stream's
 // handle last, and returns the output tensor, or the sc_status of a refused call.
+//
+// No operator here has a gradient, so a tensor that asks for one is refused while gradients are recorded
+// (its call would leave the graph without a word), and tensors written in place count their versions.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <sstream>
@@ -26,7 +30,17 @@ using Shape = at::IntArrayRef;
 
 const Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) refuse(std::string(name) + " must be a tensor");
-  return THPVariable_Unpack(o);
+  const Tensor& t = THPVariable_Unpack(o);
+  if (t.requires_grad() && c10::GradMode::is_enabled())
+    refuse(std::string(name) + " requires a gradient, and this operator has none: call it under torch.no_grad()");
+  return t;
+}
+
+// The caller's tensor o (or None) has been written by a launch.
+void written(PyObject* o) {
+  if (o == Py_None) return;
+  const Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
 [[noreturn]] void refuse_tensor(const Tensor& t, const char* name, at::ScalarType type, Shape shape, const char* how) {
@@ -119,7 +133,12 @@ void check(Py_ssize_t got, Py_ssize_t want) {
   if (got != want) refuse("wrong number of arguments");
 }
 
-PyObject* answer(sc_status s, const Tensor& out) { return s == SC_OK ? THPVariable_Wrap(out) : PyLong_FromLong(s); }
+PyObject* answer(sc_status s, const Tensor& out, PyObject* given_out, PyObject* final_state) {
+  if (s != SC_OK) return PyLong_FromLong(s);
+  written(given_out);
+  written(final_state);
+  return THPVariable_Wrap(out);
+}
 
 // x, weight, bias, silu, lengths, slots, initial_state, final_state, out, axes of x, stream
 PyObject* causal_conv(PyObject* const* v, Py_ssize_t n) {
@@ -143,7 +162,7 @@ PyObject* causal_conv(PyObject* const* v, Py_ssize_t n) {
   a.x = x.data_ptr(), a.out = out.data_ptr();
   a.x_batch = x.stride(0), a.x_channel = x.stride(1), a.out_batch = out.stride(0), a.out_channel = out.stride(1);
   a.dtype = c.dtype(), a.B = c.size(B), a.D = c.size(D), a.L = c.size(L), a.K = c.size(K);
-  return answer(sparseconv_causal_conv(&a, PyLong_AsVoidPtr(v[10])), out);
+  return answer(sparseconv_causal_conv(&a, PyLong_AsVoidPtr(v[10])), out, v[8], v[7]);
 }
 
 // x, dt, A, B, C, D, z, dt_bias, softplus, lengths, slots, initial_state, final_state, out, workspace, axes of x, stream
@@ -191,7 +210,7 @@ PyObject* selective_scan(PyObject* const* v, Py_ssize_t n) {
   if (const sc_status s = sparseconv_selective_scan_workspace(&a, &need)) return PyLong_FromLong(s);
   const Tensor ws = c.workspace(v[14], need);
   if (need) a.workspace = ws.data_ptr(), a.workspace_bytes = (int64_t)ws.nbytes();
-  return answer(sparseconv_selective_scan(&a, PyLong_AsVoidPtr(v[16])), out);
+  return answer(sparseconv_selective_scan(&a, PyLong_AsVoidPtr(v[16])), out, v[13], v[12]);
 }
 
 // x, down, up, index, scale, base, out, workspace, stream
@@ -224,7 +243,7 @@ PyObject* adapter_apply(PyObject* const* v, Py_ssize_t n) {
   if (const sc_status s = sparseconv_adapter_workspace(&a, &need)) return PyLong_FromLong(s);
   const Tensor ws = c.workspace(v[7], need);
   if (need) a.workspace = ws.data_ptr(), a.workspace_bytes = (int64_t)ws.nbytes();
-  return answer(sparseconv_adapter_apply(&a, PyLong_AsVoidPtr(v[8])), out);
+  return answer(sparseconv_adapter_apply(&a, PyLong_AsVoidPtr(v[8])), out, v[6], Py_None);
 }
 
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>

@@ -6,7 +6,8 @@ names take the packed argument structure; ``causal_conv``, ``causal_conv_step``,
 ``selective_scan``, ``selective_scan_step`` and ``adapter_apply`` take torch tensors through the
 native binding (csrc/binding.cpp), which checks their types, shapes and strides and allocates what is
 not given: ValueError where a tensor does not fit, SparseConvError where the library refuses the
-call.  Nothing is differentiable.
+call.  Nothing is differentiable: a tensor that requires a gradient is refused unless gradients are
+off (torch.no_grad()).
 
 Sequence tensors are (batch, channels, positions) with contiguous positions; batch and channel
 strides are free, so slices of a projection's output are taken as they are.  The ``_step``

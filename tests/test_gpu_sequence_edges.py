@@ -235,3 +235,55 @@ def test_empty_pools_are_refused():
     idle = _ints([0, 5])
     assert not sc.causal_conv(x, w, slots=idle, initial_state=cs, final_state=cs).any()
     assert not sc.selective_scan_step(x[..., 0], hs, x[..., 0], A, bc[..., 0], bc[..., 0], slots=idle).any()
+
+
+# ---- gradients
+
+
+def _calls(x, w, A, bc, down, up, idx, cs, hs, out):
+    """Every operator, one tensor of each kind a call."""
+    x1, bc1 = x[..., 0], bc[..., 0]
+    return {"x": lambda: sc.causal_conv(x, w), "weight": lambda: sc.causal_conv(x, w), "state": lambda: sc.causal_conv_step(x1, cs, w),
+            "out": lambda: sc.causal_conv(x, w, out=out), "A": lambda: sc.selective_scan(x, x, A, bc, bc),
+            "B": lambda: sc.selective_scan(x, x, A, bc, bc), "scan state": lambda: sc.selective_scan_step(x1, hs, x1, A, bc1, bc1),
+            "down": lambda: sc.adapter_apply(x, down, up, idx), "up": lambda: sc.adapter_apply(x, down, up, idx)}
+
+
+@pytest.mark.parametrize("which", ["x", "weight", "state", "out", "A", "B", "scan state", "down", "up"])
+def test_tensors_that_require_gradients_are_refused(which):
+    """Nothing here has a gradient: a call that a graph would have to record is refused, and runs under no_grad."""
+    t = dict(x=torch.ones(2, 8, 16), w=torch.ones(8, 4), A=-torch.ones(8, 4), bc=torch.ones(2, 1, 4, 16), down=torch.ones(1, 2, 8),
+             up=torch.ones(1, 8, 2), idx=torch.zeros(2, dtype=torch.int32), cs=torch.zeros(2, 8, 3), hs=torch.zeros(2, 8, 4),
+             out=torch.zeros(2, 8, 16))
+    t = {k: v.cuda() for k, v in t.items()}
+    call = _calls(**t)[which]
+    want = call().clone()
+    t["cs"].zero_(), t["hs"].zero_()
+    key = {"weight": "w", "state": "cs", "B": "bc", "scan state": "hs"}.get(which, which)
+    t[key].requires_grad_()
+    before = t["cs"].detach().clone(), t["hs"].detach().clone()
+    with pytest.raises(ValueError, match="gradient"):
+        call()
+    assert torch.equal(t["cs"], before[0]) and torch.equal(t["hs"], before[1])
+    with torch.no_grad():
+        assert torch.equal(call(), want)
+    with torch.inference_mode():
+        t["cs"].zero_(), t["hs"].zero_()
+        assert torch.equal(call(), want)
+
+
+def test_tensors_written_in_place_count_their_versions():
+    x, w, A = torch.ones(2, 8, 16, device="cuda"), torch.ones(8, 4, device="cuda"), -torch.ones(8, 4, device="cuda")
+    bc = torch.ones(2, 1, 4, 16, device="cuda")
+    cs, hs, out = torch.zeros(2, 8, 3, device="cuda"), torch.zeros(2, 8, 4, device="cuda"), torch.zeros(2, 8, 16, device="cuda")
+    down, up = torch.ones(1, 2, 8, device="cuda"), torch.ones(1, 8, 2, device="cuda")
+    for call, written in ((lambda: sc.causal_conv_step(x[..., 0], cs, w), [cs]),
+                          (lambda: sc.causal_conv(x, w, initial_state=cs, final_state=cs, out=out), [cs, out]),
+                          (lambda: sc.selective_scan(x, x, A, bc, bc, final_state=hs, out=out), [hs, out]),
+                          (lambda: sc.selective_scan_step(x[..., 0], hs, x[..., 0], A, bc[..., 0], bc[..., 0]), [hs]),
+                          (lambda: sc.adapter_apply(x, down, up, _ints([0, 0]), base=out, out=out), [out])):
+        read = [x, w, A, bc, down, up]
+        before = [t._version for t in written], [t._version for t in read]
+        call()
+        assert all(t._version > v for t, v in zip(written, before[0]))
+        assert [t._version for t in read] == before[1]
