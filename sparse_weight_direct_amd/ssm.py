@@ -37,10 +37,24 @@ def _adapt(which, x, base, index):
     return base
 
 
+def _fits(which, u, B, inputs, outputs, index):
+    """Refuses what adapter_apply would refuse of an adapter, before the call that uses it has written any state:
+    the same call over no positions, and what such a call does not look at."""
+    if which is None:
+        return
+    down, up, scale = which
+    if index is None:
+        raise ValueError("adapters need index, each request's adapter")
+    adapter_apply(u.new_empty(B, inputs, 0), down, up, index, scale=scale, base=u.new_empty(B, outputs, 0))
+    if down.data_ptr() % 16 or up.data_ptr() % 16:
+        raise ValueError("an adapter's down and up must be 16-byte aligned")
+
+
 class StateSpaceLayer:
     """in_proj (2 D, C), x_proj (R + 2 N, D), dt_proj (D, R), out_proj (C, D): pruned float32 weights
     on the host (zeros are not stored).  conv_weight (D, K), conv_bias (D,), A (D, N), skip (D,),
-    dt_bias (D,): float32 on the GPU."""
+    dt_bias (D,): float32 on the GPU, contiguous (conv_bias, skip and dt_bias may be None).  A call that is
+    refused leaves the states as they are."""
 
     def __init__(self, in_proj, x_proj, dt_proj, out_proj, conv_weight, conv_bias, A, skip, dt_bias, *, length: int,
                  slots: int):
@@ -53,10 +67,21 @@ class StateSpaceLayer:
         for name, w in weights.items():
             if tuple(w.shape) != shapes[name]:
                 raise ValueError(f"{name} shape {tuple(w.shape)} is not {shapes[name]}")
+        params = dict(conv_weight=(conv_weight, (self.D, conv_weight.shape[-1])), conv_bias=(conv_bias, (self.D,)),
+                      A=(A, (self.D, self.N)), skip=(skip, (self.D,)), dt_bias=(dt_bias, (self.D,)))
+        for name, (t, shape) in params.items():
+            if t is None and name in ("conv_bias", "skip", "dt_bias"):
+                continue
+            if tuple(t.shape) != shape or t.dtype != torch.float32 or t.device != A.device or not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous float32 tensor of shape {shape} on A's GPU")
+        if not 1 <= conv_weight.shape[1] <= 8 or self.N > 256:
+            raise ValueError("at most 8 taps of the convolution and 256 states")
         self.length = length
         self._prompt, self._token = ({n: Handle.from_dense(np.ascontiguousarray(w, np.float32)[:, :, None, None], 1, W, 1, 0)
                                       for n, w in weights.items()} for W in (length, 1))
-        self.conv_weight, self.conv_bias, self.A, self.skip, self.dt_bias = conv_weight, conv_bias, A, skip, dt_bias
+        # detached: the layer has no gradient, and its operators refuse tensors that ask for one
+        self.conv_weight, self.conv_bias, self.A, self.skip, self.dt_bias = (
+            None if t is None else t.detach() for t, _ in params.values())
         dev = A.device
         self.conv_state = torch.zeros(slots, self.D, conv_weight.shape[1] - 1, device=dev)
         self.scan_state = torch.zeros(slots, self.D, self.N, device=dev)
@@ -67,6 +92,7 @@ class StateSpaceLayer:
         if u.dim() != 3 or u.shape[1:] != (self.C, self.length):
             raise ValueError(f"input shape {tuple(u.shape)} is not (B, {self.C}, {self.length})")
         a = adapters or Adapters()
+        _fits(a.out_proj, u, u.shape[0], self.D, self.C, index)
 
         def project(name, x):
             return self._prompt[name].forward(x.contiguous().unsqueeze(2)).squeeze(2)
@@ -86,6 +112,7 @@ class StateSpaceLayer:
         if u.dim() != 2 or u.shape[1] != self.C:
             raise ValueError(f"input shape {tuple(u.shape)} is not (B, {self.C})")
         a = adapters or Adapters()
+        _fits(a.out_proj, u, u.shape[0], self.D, self.C, index)
 
         def project(name, x):
             return self._token[name].forward(x.contiguous()[:, :, None, None])[:, :, :, 0]

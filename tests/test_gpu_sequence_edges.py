@@ -287,3 +287,63 @@ def test_tensors_written_in_place_count_their_versions():
         call()
         assert all(t._version > v for t, v in zip(written, before[0]))
         assert [t._version for t in read] == before[1]
+
+
+# ---- the state space layer: nothing is written by a refused call
+
+
+def _layer():
+    from test_gpu_ssm import SLOTS, L, _weights
+    from sparse_weight_direct_amd.ssm import StateSpaceLayer
+    host, dev, ad, r = _weights(3)
+    m = StateSpaceLayer(host["in_proj"], host["x_proj"], host["dt_proj"], host["out_proj"], **dev, length=L, slots=SLOTS)
+    m.conv_state.copy_(r(*m.conv_state.shape)), m.scan_state.copy_(r(*m.scan_state.shape))
+    return m, ad, r, host, dev
+
+
+def test_refused_layer_calls_leave_the_states():
+    from test_gpu_ssm import C, L
+    from sparse_weight_direct_amd.ssm import Adapters
+    m, ad, r, _, _ = _layer()
+    u, slots, good = r(2, C, L), _ints([1, 4]), _ints([0, 2])
+    down, up, scale = ad.out_proj
+    only = Adapters(out_proj=ad.out_proj)
+    bad = [(only, None), (only, good.long()), (only, good[:1]), (only, good.cpu()), (only, [0, 1]),
+           (Adapters(out_proj=(down[:, :, 1:].contiguous(), up, scale)), good), (Adapters(out_proj=(down, up[:, 1:].contiguous(), scale)), good),
+           (Adapters(out_proj=(down, up[:1].contiguous(), scale)), good), (Adapters(out_proj=(down.half(), up, scale)), good),
+           (Adapters(out_proj=(down, up, torch.ones(2, device="cuda"))), good), (Adapters(out_proj=(down, up.transpose(1, 2), scale)), good),
+           (Adapters(out_proj=(down[0], up[0], scale)), good), (Adapters(out_proj=(down.cpu(), up, scale)), good),
+           (Adapters(out_proj=(down.repeat(1, 33, 1), up.repeat(1, 1, 33), scale)), good),
+           (Adapters(out_proj=(r(4 * 3 * down.shape[2] + 1)[1:].view(3, 4, -1), up, scale)), good),  # not 16-byte aligned
+          
+           (Adapters(in_proj=ad.out_proj), good)]
+    before = m.conv_state.clone(), m.scan_state.clone()
+    for adapters, index in bad:
+        for call in (lambda: m.step(u[:, :, 0], slots, adapters=adapters, index=index),
+                     lambda: m.prompt(u, slots, resume=True, adapters=adapters, index=index)):
+            with pytest.raises((ValueError, sc.SparseConvError)):
+                call()
+            assert torch.equal(m.conv_state, before[0]) and torch.equal(m.scan_state, before[1])
+    m.step(u[:, :, 0], slots, adapters=only, index=good)  # and the right call runs
+    assert not torch.equal(m.conv_state, before[0])
+
+
+def test_layer_parameters_are_checked_at_once():
+    from test_gpu_ssm import SLOTS, L, D
+    from sparse_weight_direct_amd.ssm import StateSpaceLayer
+    _, _, _, host, dev = _layer()
+    w = (host["in_proj"], host["x_proj"], host["dt_proj"], host["out_proj"])
+    for name, v in (("skip", dev["skip"][1:]), ("dt_bias", dev["dt_bias"].half()), ("conv_bias", dev["conv_bias"].cpu()),
+                    ("A", dev["A"].double()), ("conv_weight", dev["conv_weight"][: D // 2]), ("conv_weight", dev["conv_weight"].t())):
+        with pytest.raises(ValueError):
+            StateSpaceLayer(*w, **{**dev, name: v}, length=L, slots=SLOTS)
+
+
+def test_layer_takes_parameters_that_require_gradients():
+    from test_gpu_ssm import C, L, SLOTS
+    from sparse_weight_direct_amd.ssm import StateSpaceLayer
+    m, _, r, host, dev = _layer()
+    same = StateSpaceLayer(host["in_proj"], host["x_proj"], host["dt_proj"], host["out_proj"], length=L, slots=SLOTS,
+                           **{k: torch.nn.Parameter(v) for k, v in dev.items()})
+    u, slots = r(2, C, L), _ints([1, 4])
+    assert torch.equal(m.prompt(u, slots), same.prompt(u, slots)) and torch.equal(m.scan_state[slots.long()], same.scan_state[slots.long()])
