@@ -22,11 +22,23 @@ import torch
 
 from . import LIB_PATH, SparseConvError, _check, _i32, _lib, _stream_ptr, _vp
 
+
+
+class _NoBinding:
+    """Stands for a binding that is missing or does not load: the rest of the package does not need it."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{name} needs _binding.so beside {LIB_PATH}, which is missing or does not load ({self._why}): build it "
+                          "with `python -c 'import __graft_entry__ as g; g.build()'`")
+
+
 try:
     from . import _binding
 except ImportError as e:
-    raise ImportError(f"_binding.so beside {LIB_PATH} is missing or does not load: build it with "
-                      "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+    _binding = _NoBinding(str(e))
 
 SC_F32, SC_BF16, SC_F16 = range(3)
 SC_SEQ_SILU, SC_SEQ_SOFTPLUS = 1, 2
