@@ -10,20 +10,21 @@
 #include <hip/hip_runtime.h>
 
 #include "sequence_device.h"
+#include "sequence_plan.h"
 
 namespace sc {
 
 namespace {
 
-constexpr int kV = 8;  // positions per thread: at least K - 1, so only a row's first thread meets the state
+constexpr int kV = kConvV;  // positions per thread
 
 // A thread makes kV positions of one row from them and the kV before them (the second read comes from
 // L1).  ROW: a workgroup stays in one row (of `blocks` workgroups), so everything but the positions is
-// scalar; otherwise, for rows that would leave its threads idle, each thread has a place of its own.
+// scalar; otherwise, for rows that would leave its threads idle, each thread has a place of its own.  (L may be
+// 2^31 - 1: nothing here may pass it, and t0 is compared by what is left of the row.)
 template <class T, int K, bool SILU, bool ROW>
-__global__ __launch_bounds__(256) void causal_conv_rows(const sc_causal_conv a, int blocks) {
+__global__ __launch_bounds__(256) void causal_conv_rows(const sc_causal_conv a, int blocks, int nv) {
   typedef typename Pack<T, kV>::type Vec;
-  const int nv = max(1, (a.L + kV - 1) / kV);
   int row, t0;
   if (ROW) {
     row = blockIdx.x / blocks;
@@ -84,14 +85,14 @@ __global__ __launch_bounds__(256) void causal_conv_rows(const sc_causal_conv a, 
     for (int k = 0; k < K; k++) v = fmaf(w[k], f[i + k], v);
     y[i] = T(SILU ? silu(v) : v);
   }
-  if (t0 + kV > len)
+  if (len - t0 < kV)
 #pragma unroll
     for (int i = 0; i < kV; i++) y[i] = t0 + i < len ? y[i] : T(0.0f);
   store_some<T, kV>(static_cast<T*>(a.out) + b * a.out_batch + d * a.out_channel + t0, here, y);
 }
 
 // Single positions: a thread takes kC channels, whose states lie together.
-constexpr int kC = 4;
+constexpr int kC = kConvC;
 
 template <class T, int K, bool SILU>
 __global__ __launch_bounds__(256) void causal_conv_token(const sc_causal_conv a, int per_row) {
@@ -154,21 +155,21 @@ __global__ __launch_bounds__(256) void causal_conv_token(const sc_causal_conv a,
 template <class T, int K, bool SILU>
 int launch_one(const sc_causal_conv& a, hipStream_t st) {
   if (a.L == 1) {
-    const int per_row = (a.D + kC - 1) / kC;
+    const int per_row = (int)ceil_div(a.D, kC);
     hipLaunchKernelGGL((causal_conv_token<T, K, SILU>), dim3((unsigned)(((int64_t)a.B * per_row + 255) / 256)), dim3(256), 0,
                        st, a, per_row);
     return (int)hipGetLastError();
   }
-  const int nv = std::max(1, (a.L + kV - 1) / kV), blocks = (nv + 255) / 256;
+  const int nv = (int)conv_places(a), blocks = (nv + 255) / 256;
   const int64_t rows = (int64_t)a.B * a.D;
   // Rows that keep 4/5 (fp32: 2/3) of a workgroup busy get workgroups of their own (2048 positions, bf16: 29.4 instead of
   // 30.4 us for 8 x 2048 rows, fp32 11.9 instead of 14.0 for 5 x 1000 of 1537); with less the idle threads cost
   // more (2500 positions, bf16, 4 x 2048 rows: 27.2 instead of 20.8 us).
   if (blocks * 256 * 4 <= (sizeof(T) == 4 ? 6 : 5) * nv)
-    hipLaunchKernelGGL((causal_conv_rows<T, K, SILU, true>), dim3((unsigned)(rows * blocks)), dim3(256), 0, st, a, blocks);
+    hipLaunchKernelGGL((causal_conv_rows<T, K, SILU, true>), dim3((unsigned)(rows * blocks)), dim3(256), 0, st, a, blocks, nv);
   else
     hipLaunchKernelGGL((causal_conv_rows<T, K, SILU, false>), dim3((unsigned)((rows * nv + 255) / 256)), dim3(256), 0, st, a,
-                       blocks);
+                       blocks, nv);
   return (int)hipGetLastError();
 }
 

@@ -7,6 +7,7 @@
 #include <string>
 
 #include "sequence.h"
+#include "sequence_plan.h"
 
 namespace {
 
@@ -141,7 +142,7 @@ sc_status sparseconv_causal_conv(const sc_causal_conv* a, void* hip_stream) {
     if ((a->flags & ~SC_SEQ_SILU) || a->reserved) return fail(SC_EINVAL, "unknown flag, or reserved is not 0");
     if (a->B < 0 || a->L < 0 || a->D < 1 || a->K < 1) return fail(SC_ESHAPE, "B, L >= 0 and D, K >= 1");
     if (a->K > 8) return fail(SC_EUNSUPPORTED, "K > 8");
-    if ((long double)a->B * a->D * std::max(1, a->L / 8 + 1) >= 2147483648.0L)
+    if (!sc::conv_fits(*a))
       return fail(SC_EUNSUPPORTED, "B*D*ceil(L/8) >= 2^31");
     if (a->B == 0) return SC_OK;
     const int64_t es = size_of(a->dtype), per = (int64_t)a->D * (a->K - 1);

@@ -167,3 +167,18 @@ def test_the_binding_refuses_host_tensors():
               lambda: sc.selective_scan(x, x, w, x, x), lambda: sc.adapter_apply(x, x, x, x), lambda: sc.causal_conv([1.0], w)):
         with pytest.raises(ValueError):
             f()
+
+
+def test_conv_limit_is_the_documented_one():
+    """B * D * ceil(L / 8) < 2^31, to the last row.  (Accepted calls end at the device: SC_EDEVICE where there is none.)"""
+    import torch
+    far = dict(x=1 << 44, out=1 << 45, weight=1 << 42, bias=0, initial=0, final=0, lengths=0, num_slots=1 << 30)
+
+    def status(B, D, L):
+        return _status(sc.sparseconv_causal_conv, _conv(B=B, D=D, L=L, x_channel=L, out_channel=L, x_batch=D * L, out_batch=D * L,
+                                                        **far))
+    assert status(8, 1, (1 << 31) - 1) == EUNSUPPORTED and status(1 << 14, 1 << 14, 64) == EUNSUPPORTED
+    assert status(1 << 15, 1 << 16, 1) == EUNSUPPORTED
+    if not torch.cuda.is_available():
+        for B, D, L in ((7, 1, (1 << 31) - 1), (1, 7, (1 << 31) - 7), ((1 << 14) - 1, 1 << 14, 64), ((1 << 15) - 1, 1 << 16, 1)):
+            assert status(B, D, L) == sc.SC_EDEVICE
