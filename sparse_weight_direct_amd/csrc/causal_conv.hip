@@ -100,7 +100,7 @@ __global__ __launch_bounds__(256) void causal_conv_token(const sc_causal_conv a,
   const uint32_t id = blockIdx.x * 256u + threadIdx.x;
   const int b = id / (uint32_t)per_row, d = (id - (uint32_t)b * per_row) * kC;
   if (b >= a.B) return;
-  const int slot = slot_of(a.slots, a.num_slots, b), n = a.D - d;
+  const int slot = slot_of(a.slots, a.num_slots, b), n = min(a.D - d, kC);
   const bool on = slot >= 0 && length_of(a.lengths, 1, b) == 1;
   const T* x = static_cast<const T*>(a.x) + b * a.x_batch + d * a.x_channel;
   T* out = static_cast<T*>(a.out) + b * a.out_batch + d * a.out_channel;
