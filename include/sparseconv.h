@@ -476,7 +476,9 @@ typedef struct {
  *     h_t[n] = exp(s_t A[d,n]) h_{t-1}[n] + s_t b_t[n] x_t,   s_t = dt_t + dt_bias[d] (softplus of it with
  *     out_t  = (sum_n c_t[n] h_t[n] + skip[d] x_t) z_t sigmoid(z_t)                    SC_SEQ_SOFTPLUS)
  * (without z, out_t is the first factor).  b, c: strides in elements, positions contiguous; with
- * L = 1 the states' stride may be any.  B, L >= 0.  Limits: B*D < 2^31, L < 2^30.  Meant for
+ * L = 1 the states' stride may be any.  B, L >= 0.  Limits: B*D < 2^31, L < 2^30, and fewer than 2^24
+ * workgroups, B*G*ceil(D/G/16) of them (with L = 1 one for 256 channels of a group, or 128 and 64 with more than
+ * 16 and 32 states, and D/G <= 2^31 - 257).  Meant for
  * s_t A <= 0 (states that decay): 256 positions are composed through the product of their
  * exponentials, so growth beyond fp32's range within them is not finite.
  */

@@ -14,6 +14,7 @@
 #include <algorithm>
 
 #include "sequence_device.h"
+#include "sequence_plan.h"
 
 namespace sc {
 
@@ -37,7 +38,7 @@ namespace {
 // channels the axis is cut in segments: a first pass makes each segment's end state from 0 (no outputs,
 // no c), the second composes the ends before its segment and walks it.
 
-constexpr int kRows = 16;    // channels per workgroup
+constexpr int kRows = kScanRows;  // channels per workgroup
 constexpr int kStates = 16;  // states of b and c in LDS at a time
 
 // Pitch of a channel's {A, h} in LDS: one past N, so that the four channels of a wavefront read other banks.
@@ -417,7 +418,7 @@ __global__ __launch_bounds__(256) void scan_token(const sc_selective_scan a, int
 
 template <class T, int Q>
 int launch_token(const sc_selective_scan& a, hipStream_t st) {
-  const int per = 4 * (256 / Q), blocks = (a.D / a.G + per - 1) / per;
+  const int blocks = (int)ceil_div(a.D / a.G, 4 * (256 / Q));
   const dim3 grid((unsigned)((int64_t)a.B * a.G * blocks));
   if (a.N % 4 == 0 && a.b_state == 1 && a.c_state == 1)
     hipLaunchKernelGGL((scan_token<T, Q, true>), grid, dim3(256), 0, st, a, blocks);
@@ -426,53 +427,8 @@ int launch_token(const sc_selective_scan& a, hipStream_t st) {
   return (int)hipGetLastError();
 }
 
-// How a prompt's scan is cut.  Measured with 16 states, bf16, us, one sequence of D channels and L positions:
-//
-//   segments   D 512, L 8192   D 1024, L 1024   D 2048, L 8192   D 4096, L 2048
-//      1            256             34.5             268              70.8
-//      4            121             20.8             163              71.7
-//     16             50                              139
-//
-// so the axis is cut where fewer than 5/8 of the CUs have a workgroup, into 4 workgroups a CU or single
-// chunks; two segments cost what they save (two chunks: 18.4 and 19.5 us).  Reading ahead takes registers
-// that a fourth wavefront a SIMD could use: with up to 2 workgroups a CU it gains (D 4096, L 1024: 46.7 ->
-// 37.9 us), with 4 it loses (4 x 4096 x 2048: 166 -> 181 us).
-//
-// Positions a lane (a chunk is 16 lanes of them); a chunk that is not whole is padded and takes the guarded loads:
-//
-//   B x D       a lane   L 160   L 256   L 300   L 384   L 520
-//   8 x 4096      16      46.4    43.4    87.1    84.5   125.7
-//                  8      45.2    43.8    67.8    65.2   107.5
-//   1 x 4096      16      14.6    11.1    25.5    23.7    32.8
-//                  8      13.7    12.6    20.8    19.7    32.1
-//   1 x 1024      16      14.3    10.8    24.6    22.0    24.3
-//                  8      13.4    12.4    19.4    17.2    27.9
-//
-// so eight up to 384 positions unless they fill a chunk of sixteens; above, the two change places with every chunk.
-struct Plan {
-  int ti, chunks, segments;  // positions per lane
-  int64_t groups;            // workgroups of a segment
-  bool ahead;
-};
-
-Plan plan_of(const sc_selective_scan& a, int cus) {
-  Plan p;
-  const bool eight = a.L <= 384 && a.L != 256;
-  p.ti = a.L <= 64 ? 4 : eight || a.N > 239 ? 8 : 16;  // beyond 239 states 16 would pass 64 KB of LDS
-  const int64_t share = a.D / a.G;
-  p.groups = (int64_t)a.B * a.G * ((share + kRows - 1) / kRows);
-  const int chunks = std::max(1, (a.L + 16 * p.ti - 1) / (16 * p.ti));
-  int segments = 1;
-  if (p.ti == 16 && 8 * p.groups <= 5 * cus) segments = (int)std::min<int64_t>(std::min(chunks, 64), (4 * cus + p.groups - 1) / p.groups);
-  if (segments < 3) segments = 1;
-  p.chunks = (chunks + segments - 1) / segments;
-  p.segments = (chunks + p.chunks - 1) / p.chunks;
-  p.ahead = p.ti == 16 && p.groups * p.segments <= 2 * cus;
-  return p;
-}
-
 template <class T, int TI, bool ENDS, bool AHEAD>
-int launch_part(const sc_selective_scan& a, const Plan& p, const Split& sp, hipStream_t st) {
+int launch_part(const sc_selective_scan& a, const ScanPlan& p, const Split& sp, hipStream_t st) {
   const int lds = ((ENDS ? 1 : 2) * kStates * 16 * TI + (kRows + 1) * ah_pitch(a.N) * 2) * 4;
   const int64_t blocks = p.groups * (ENDS ? p.segments - 1 : p.segments);
   hipLaunchKernelGGL((scan_prompt<T, TI, ENDS, AHEAD>), dim3((unsigned)blocks), dim3(256), lds, st, a, sp);
@@ -480,7 +436,7 @@ int launch_part(const sc_selective_scan& a, const Plan& p, const Split& sp, hipS
 }
 
 template <class T>
-int launch_prompt(const sc_selective_scan& a, const Plan& p, hipStream_t st) {
+int launch_prompt(const sc_selective_scan& a, const ScanPlan& p, hipStream_t st) {
   Split sp{p.segments, p.chunks, nullptr, nullptr};
   if (p.ti == 4) return launch_part<T, 4, false, false>(a, p, sp, st);
   if (p.ti == 8) return launch_part<T, 8, false, false>(a, p, sp, st);
@@ -495,18 +451,20 @@ int launch_prompt(const sc_selective_scan& a, const Plan& p, hipStream_t st) {
 template <class T>
 int launch_type(const sc_selective_scan& a, int cus, hipStream_t st) {
   if (a.L == 1) {
-    if (a.N <= 16) return launch_token<T, 4>(a, st);
-    if (a.N <= 32) return launch_token<T, 8>(a, st);
-    return launch_token<T, 16>(a, st);
+    switch (scan_token_lanes(a.N)) {
+      case 4: return launch_token<T, 4>(a, st);
+      case 8: return launch_token<T, 8>(a, st);
+      default: return launch_token<T, 16>(a, st);
+    }
   }
-  return launch_prompt<T>(a, plan_of(a, cus), st);
+  return launch_prompt<T>(a, scan_plan(a, cus), st);
 }
 
 }  // namespace
 
 int64_t scan_workspace(const sc_selective_scan& a, int cus) {
   if (a.L <= 1) return 0;
-  const Plan p = plan_of(a, cus);
+  const ScanPlan p = scan_plan(a, cus);
   return p.segments == 1 ? 0 : (int64_t)a.B * p.segments * a.D * (a.N + 1) * 4;
 }
 

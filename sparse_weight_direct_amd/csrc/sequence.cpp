@@ -114,6 +114,7 @@ sc_status check_scan_sizes(const sc_selective_scan* a) {
   if (a->D % a->G) return fail(SC_ESHAPE, "G does not divide D");
   if (a->N > 256) return fail(SC_EUNSUPPORTED, "N > 256");
   if ((int64_t)a->B * a->D >= (1LL << 31) || a->L >= (1 << 30)) return fail(SC_EUNSUPPORTED, "B*D >= 2^31 or L >= 2^30");
+  if (!sc::scan_fits(*a)) return fail(SC_EUNSUPPORTED, "more workgroups than a launch holds");
   return SC_OK;
 }
 

@@ -9,6 +9,9 @@
 
 namespace sc {
 
+// Threads of a launch: the device counts them in 32 bits.
+constexpr int64_t kGridThreads = 1LL << 32;
+
 constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // ---- Causal convolution: a thread makes kConvV positions of a row, or kConvC channels of a single position.
@@ -20,5 +23,64 @@ inline int64_t conv_places(const sc_causal_conv& a) { return std::max<int64_t>(1
 
 // The limit on its sizes: fewer than 2^31 of them (workgroups that stay in a row add less than half).
 inline bool conv_fits(const sc_causal_conv& a) { return (int64_t)a.B * a.D < (1LL << 31) && (int64_t)a.B * a.D * conv_places(a) < (1LL << 31); }
+
+// ---- Selective scan
+constexpr int kScanRows = 16;     // channels per workgroup of a prompt
+constexpr int kScanThreads = 256;
+
+// Lanes that share a channel's states at a single position, and its channels per workgroup (four a thread).
+inline int scan_token_lanes(int N) { return N <= 16 ? 4 : N <= 32 ? 8 : 16; }
+inline int64_t scan_token_channels(int N) { return 4 * (kScanThreads / scan_token_lanes(N)); }
+
+// How a prompt's scan is cut.  Measured with 16 states, bf16, us, one sequence of D channels and L positions:
+//
+//   segments   D 512, L 8192   D 1024, L 1024   D 2048, L 8192   D 4096, L 2048
+//      1            256             34.5             268              70.8
+//      4            121             20.8             163              71.7
+//     16             50                              139
+//
+// so the axis is cut where fewer than 5/8 of the CUs have a workgroup, into 4 workgroups a CU or single
+// chunks; two segments cost what they save (two chunks: 18.4 and 19.5 us).  Reading ahead takes registers
+// that a fourth wavefront a SIMD could use: with up to 2 workgroups a CU it gains (D 4096, L 1024: 46.7 ->
+// 37.9 us), with 4 it loses (4 x 4096 x 2048: 166 -> 181 us).
+//
+// Positions a lane (a chunk is 16 lanes of them); a chunk that is not whole is padded and takes the guarded loads:
+//
+//   B x D       a lane   L 160   L 256   L 300   L 384   L 520
+//   8 x 4096      16      46.4    43.4    87.1    84.5   125.7
+//                  8      45.2    43.8    67.8    65.2   107.5
+//   1 x 4096      16      14.6    11.1    25.5    23.7    32.8
+//                  8      13.7    12.6    20.8    19.7    32.1
+//   1 x 1024      16      14.3    10.8    24.6    22.0    24.3
+//                  8      13.4    12.4    19.4    17.2    27.9
+//
+// so eight up to 384 positions unless they fill a chunk of sixteens; above, the two change places with every chunk.
+struct ScanPlan {
+  int ti, chunks, segments;  // positions per lane; chunks of 16 of them per segment
+  int64_t groups;            // workgroups of a segment
+  bool ahead;
+};
+
+inline ScanPlan scan_plan(const sc_selective_scan& a, int cus) {
+  ScanPlan p;
+  const bool eight = a.L <= 384 && a.L != 256;
+  p.ti = a.L <= 64 ? 4 : eight || a.N > 239 ? 8 : 16;  // beyond 239 states 16 would pass 64 KB of LDS
+  p.groups = (int64_t)a.B * a.G * ceil_div(a.D / a.G, kScanRows);
+  const int chunks = std::max(1, (a.L + 16 * p.ti - 1) / (16 * p.ti));
+  int segments = 1;
+  if (p.ti == 16 && 8 * p.groups <= 5 * cus) segments = (int)std::min<int64_t>(std::min(chunks, 64), (4 * cus + p.groups - 1) / p.groups);
+  if (segments < 3) segments = 1;
+  p.chunks = (chunks + segments - 1) / segments;
+  p.segments = (chunks + p.chunks - 1) / p.chunks;
+  p.ahead = p.ti == 16 && p.groups * p.segments <= 2 * cus;
+  return p;
+}
+
+// Whether a launch holds its threads (cutting the axis makes no more of them than a few a CU) and a channel's
+// number, counted up to the workgroup's end, stays in 32 bits.
+inline bool scan_fits(const sc_selective_scan& a) {
+  const int64_t share = a.D / a.G, per = a.L == 1 ? scan_token_channels(a.N) : kScanRows;
+  return share + per < (1LL << 31) && (int64_t)a.B * a.G * ceil_div(share, per) * kScanThreads < kGridThreads;
+}
 
 }  // namespace sc

@@ -182,3 +182,31 @@ def test_conv_limit_is_the_documented_one():
     if not torch.cuda.is_available():
         for B, D, L in ((7, 1, (1 << 31) - 1), (1, 7, (1 << 31) - 7), ((1 << 14) - 1, 1 << 14, 64), ((1 << 15) - 1, 1 << 16, 1)):
             assert status(B, D, L) == sc.SC_EDEVICE
+
+
+def _far_scan(B, D, L, N, G):
+    """A scan of dense tensors that lie apart; the workspace is what it asks for."""
+    kw = dict(B=B, D=D, L=L, N=N, G=G, z=0, skip=0, dt_bias=0, lengths=0, slots=0, initial=0, final=0, num_slots=B,
+              x=1 << 44, dt=2 << 44, b=3 << 44, c=4 << 44, out=5 << 44, A=6 << 44, workspace=7 << 44, workspace_bytes=1 << 40)
+    for k in ("x", "dt", "z", "out"):
+        kw |= {k + "_channel": L, k + "_batch": D * L}
+    for k in ("b", "c"):
+        kw |= {k + "_state": L, k + "_group": N * L, k + "_batch": G * N * L}
+    return _scan(**kw)
+
+
+def test_scan_launches_fit_the_grid():
+    """2^24 workgroups are more threads than a launch holds: refused before it, and by the workspace query.  What
+    single positions take fewer workgroups for stays accepted.  (SC_EDEVICE: a call that got past the checks.)"""
+    import torch
+    for B, D, L, N, G in ((1 << 12, 1 << 12, 5, 4, 1 << 12), (1 << 16, 1 << 12, 2, 4, 1), (1 << 24, 3, 7, 16, 1),
+                          (1 << 12, 1 << 12, 1, 4, 1 << 12), (1 << 24, 64, 1, 64, 1), (1 << 17, 1 << 13, 1, 40, 1), (1, (1 << 31) - 1, 1, 1, 1)):
+        args = _far_scan(B, D, L, N, G)
+        assert _status(sc.sparseconv_selective_scan, args) == EUNSUPPORTED, (B, D, L, N, G)
+        with pytest.raises(sc.SparseConvError, match="SC_EUNSUPPORTED"):
+            sc.sparseconv_selective_scan_workspace(args)
+    if torch.cuda.is_available():
+        return
+    for B, D, L, N, G in (((1 << 12) - 1, 1 << 12, 5, 4, 1 << 12), (1 << 16, (1 << 12) - 16, 2, 4, 1), ((1 << 24) - 1, 3, 7, 16, 1),
+                          (1 << 16, 1 << 12, 1, 4, 1), (1 << 17, 1 << 13, 1, 30, 1), (1, (1 << 31) - 257, 1, 1, 1)):
+        assert _status(sc.sparseconv_selective_scan, _far_scan(B, D, L, N, G)) == sc.SC_EDEVICE, (B, D, L, N, G)
