@@ -507,7 +507,9 @@ typedef struct {
 /*
  * out[b] = base[b] + scale[r] * up[r] (down[r] x[b]) with r = index[b]: the low-rank adapters of
  * many requests in one call, beside a projection that they share (a packed 1x1 layer).
- * B, L >= 0, M, C, adapters >= 1.  Limits: B*C*R, B*M*R < 2^31, L < 2^30.
+ * B, L >= 0, M, C, adapters >= 1.  Limits: B*C*R, B*M*R < 2^31, L < 2^30, C, M <= 2^31 - 1024,
+ * B*ceil(L/64) < 2^23 (B*ceil(L/128) in 16-bit types), and with L < 4 (8 in 16-bit types)
+ * B*L*ceil(M/1024) < 2^23.
  */
 sc_status sparseconv_adapter_apply(const sc_adapter* a, void* hip_stream);
 

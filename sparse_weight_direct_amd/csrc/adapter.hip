@@ -12,6 +12,7 @@
 #include <algorithm>
 
 #include "sequence_device.h"
+#include "sequence_plan.h"
 #include "xcd.h"
 
 namespace sc {
@@ -353,8 +354,8 @@ __global__ __launch_bounds__(256, 4) void adapter_up(const sc_adapter a, const f
 // makes the R values for itself (down[r] comes from L2 after the first workgroup has read it), which
 // costs less than a second launch.  Its time is latency: what the second half needs (the base and the
 // first kFront values of every row of up) is asked for before the first half begins.
-constexpr int kToken = 512;   // threads
-constexpr int kTokenRows = 2;   // output channels per thread
+constexpr int kToken = kAdapterToken;          // threads
+constexpr int kTokenRows = kAdapterTokenRows;  // output channels per thread
 constexpr int kFront = 16;  // (what follows takes them in 16s too)
 
 // RW: rows of down per wavefront at a time.
@@ -461,47 +462,10 @@ __global__ __launch_bounds__(kToken) void adapter_token(const sc_adapter a, int 
   }
 }
 
-struct Plan {
-  bool token;
-  int ltiles, segments, rpieces;  // positions' tiles; pieces of C and of R
-  int mtiles, mrows;     // output channels' pieces
-  bool wide;             // second product: four tiles of positions side by side
-};
-
-Plan plan_of(const sc_adapter& a, int cus) {
-  Plan p{};
-  const bool wide = a.dtype == SC_F32;
-  p.token = a.L < (wide ? 4 : 8);  // a tile's lane holds so many positions
-  if (p.token) {
-    p.mrows = kTokenRows * kToken;
-    p.mtiles = (a.M + p.mrows - 1) / p.mrows;
-    return p;
-  }
-  p.ltiles = (a.L + (wide ? 64 : 128) - 1) / (wide ? 64 : 128);
-  const int64_t tiles = (int64_t)a.B * p.ltiles;
-  const int blocks = (a.C + (wide ? 16 : 32) - 1) / (wide ? 16 : 32);
-  p.rpieces = (a.R + 63) / 64;
-  const int nw = a.R <= 32 ? 8 : 4;
-  // 1, 2 or 4 pieces of C, so that every CU has a workgroup or two (an empty piece's sums are 0)
-  const int64_t want = 2 * cus / (tiles * p.rpieces);
-  p.segments = want >= 4 && blocks >= 4 * nw ? 4 : want >= 2 && blocks >= 2 * nw ? 2 : 1;
-  // Four wavefronts side by side read and write 1 KB of a row together instead of 256 bytes (fp32,
-  // 8 x 2048 -> 4096 x 1024: 78 -> 73 us), where that leaves few of them idle, LDS holds four tiles and
-  // there is a workgroup for every CU and more (bf16, 8 x 2048 -> 2048 x 512, 128 of them: 24.9 us against 16.4).
-  p.wide = a.R <= 16 && (p.ltiles % 4 == 0 || p.ltiles >= 12) &&
-           (int64_t)a.B * ((p.ltiles + 3) / 4) * ((a.M + 127) / 128) >= 3 * cus;
-  const int64_t sets = (int64_t)a.B * (p.wide ? (p.ltiles + 3) / 4 : p.ltiles);
-  p.mtiles = (int)std::clamp<int64_t>((4 * cus + sets - 1) / sets, 1, (a.M + 127) / 128);
-  p.mrows = ((a.M + p.mtiles - 1) / p.mtiles + 63) / 64 * 64;
-  p.mtiles = (a.M + p.mrows - 1) / p.mrows;
-  return p;
-}
-
 template <class T, int S>
-int launch_up(const sc_adapter& a, const Plan& p, int lds, const float* low, hipStream_t st) {
-  const int wl = p.wide ? 4 : 1;
-  const dim3 grid((unsigned)((int64_t)a.B * ((p.ltiles + wl - 1) / wl) * p.mtiles));
-  if (wl == 4)
+int launch_up(const sc_adapter& a, const AdapterPlan& p, int lds, const float* low, hipStream_t st) {
+  const dim3 grid((unsigned)p.up_blocks);
+  if (p.wide)
     hipLaunchKernelGGL((adapter_up<T, S, 4>), grid, dim3(256), 4 * lds, st, a, low, p.ltiles, p.mtiles, p.mrows);
   else
     hipLaunchKernelGGL((adapter_up<T, S, 1>), grid, dim3(256), lds, st, a, low, p.ltiles, p.mtiles, p.mrows);
@@ -510,17 +474,17 @@ int launch_up(const sc_adapter& a, const Plan& p, int lds, const float* low, hip
 
 template <class T>
 int launch_type(const sc_adapter& a, int cus, hipStream_t st) {
-  const Plan p = plan_of(a, cus);
+  const AdapterPlan p = adapter_plan(a, cus);
   if (p.token) {
-    const int64_t n = (int64_t)a.B * a.L * p.mtiles;
+    const dim3 grid((unsigned)p.up_blocks);
     if (a.R <= 16)
-      hipLaunchKernelGGL((adapter_token<T, 2>), dim3((unsigned)n), dim3(kToken), 0, st, a, p.mtiles, p.mrows);
+      hipLaunchKernelGGL((adapter_token<T, 2>), grid, dim3(kToken), 0, st, a, p.mtiles, p.mrows);
     else
-      hipLaunchKernelGGL((adapter_token<T, 4>), dim3((unsigned)n), dim3(kToken), 0, st, a, p.mtiles, p.mrows);
+      hipLaunchKernelGGL((adapter_token<T, 4>), grid, dim3(kToken), 0, st, a, p.mtiles, p.mrows);
     return (int)hipGetLastError();
   }
   float* low = static_cast<float*>(a.workspace);
-  const dim3 gd((unsigned)((int64_t)a.B * p.ltiles * p.segments * p.rpieces));
+  const dim3 gd((unsigned)p.down_blocks);
   if (a.R <= 16)
     hipLaunchKernelGGL((adapter_down<T, 1, 8>), gd, dim3(512), 0, st, a, low, p.segments, p.ltiles, p.rpieces);
   else if (a.R <= 32)
@@ -538,7 +502,7 @@ int launch_type(const sc_adapter& a, int cus, hipStream_t st) {
 }  // namespace
 
 int64_t adapter_workspace(const sc_adapter& a, int cus) {
-  const Plan p = plan_of(a, cus);
+  const AdapterPlan p = adapter_plan(a, cus);
   return p.token ? 0 : (int64_t)p.segments * a.B * a.R * a.L * 4;
 }
 

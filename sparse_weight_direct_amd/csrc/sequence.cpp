@@ -127,8 +127,8 @@ sc_status check_adapter_sizes(const sc_adapter* a) {
   if (a->R > 128) return fail(SC_EUNSUPPORTED, "R > 128");
   if ((int64_t)a->B * a->C * a->R >= (1LL << 31) || (int64_t)a->B * a->M * a->R >= (1LL << 31) || a->L >= (1 << 30))
     return fail(SC_EUNSUPPORTED, "B*C*R or B*M*R >= 2^31, or L >= 2^30");
-  if ((long double)a->B * (a->L / 64 + 1) * (a->M / 64 + 8) >= 2147483648.0L)
-    return fail(SC_EUNSUPPORTED, "B*L*M >= 2^43");
+  if (a->C > sc::kAdapterMost || a->M > sc::kAdapterMost) return fail(SC_EUNSUPPORTED, "C or M > 2^31 - 1024");
+  if (!sc::adapter_fits(*a)) return fail(SC_EUNSUPPORTED, "more workgroups than a launch holds");
   return SC_OK;
 }
 

@@ -83,4 +83,59 @@ inline bool scan_fits(const sc_selective_scan& a) {
   return share + per < (1LL << 31) && (int64_t)a.B * a.G * ceil_div(share, per) * kScanThreads < kGridThreads;
 }
 
+// ---- Low-rank adapters
+constexpr int kAdapterToken = 512;   // threads of a workgroup of single positions
+constexpr int kAdapterTokenRows = 2;  // output channels per thread
+constexpr int kAdapterMost = 2147483647 - 1023;  // channels: counted up to a workgroup's end in 32 bits
+
+struct AdapterPlan {
+  bool token;
+  int ltiles, segments, rpieces;  // positions' tiles; pieces of C and of R
+  int mtiles, mrows;              // output channels' pieces
+  bool wide;                      // second product: four tiles of positions side by side
+  int64_t down_blocks, up_blocks;  // workgroups of the two products (single positions: the second's alone)
+  int down_threads, up_threads;
+};
+
+// The sizes have been checked (C, M <= kAdapterMost, R <= 128, L < 2^30).
+inline AdapterPlan adapter_plan(const sc_adapter& a, int cus) {
+  AdapterPlan p{};
+  const bool wide = a.dtype == SC_F32;
+  p.token = a.L < (wide ? 4 : 8);  // a tile's lane holds so many positions
+  if (p.token) {
+    p.mrows = kAdapterTokenRows * kAdapterToken;
+    p.mtiles = (int)ceil_div(a.M, p.mrows);
+    p.up_blocks = (int64_t)a.B * a.L * p.mtiles, p.up_threads = kAdapterToken;
+    return p;
+  }
+  p.ltiles = (int)ceil_div(a.L, wide ? 64 : 128);
+  const int64_t tiles = (int64_t)a.B * p.ltiles;
+  const int blocks = (int)ceil_div(a.C, wide ? 16 : 32);
+  p.rpieces = (a.R + 63) / 64;
+  const int nw = a.R <= 32 ? 8 : 4;
+  // 1, 2 or 4 pieces of C, so that every CU has a workgroup or two (an empty piece's sums are 0)
+  const int64_t want = 2 * cus / (tiles * p.rpieces);
+  p.segments = want >= 4 && blocks >= 4 * nw ? 4 : want >= 2 && blocks >= 2 * nw ? 2 : 1;
+  p.down_blocks = tiles * p.segments * p.rpieces, p.down_threads = 64 * nw;
+  // Four wavefronts side by side read and write 1 KB of a row together instead of 256 bytes (fp32,
+  // 8 x 2048 -> 4096 x 1024: 78 -> 73 us), where that leaves few of them idle, LDS holds four tiles and
+  // there is a workgroup for every CU and more (bf16, 8 x 2048 -> 2048 x 512, 128 of them: 24.9 us against 16.4).
+  const int64_t mmost = ceil_div(a.M, 128);
+  p.wide = a.R <= 16 && (p.ltiles % 4 == 0 || p.ltiles >= 12) && (int64_t)a.B * ceil_div(p.ltiles, 4) * mmost >= 3 * cus;
+  const int64_t sets = (int64_t)a.B * (p.wide ? ceil_div(p.ltiles, 4) : p.ltiles);
+  p.mtiles = (int)std::clamp<int64_t>((4 * cus + sets - 1) / sets, 1, mmost);
+  p.mrows = (int)ceil_div(ceil_div(a.M, p.mtiles), 64) * 64;
+  p.mtiles = (int)ceil_div(a.M, p.mrows);
+  p.up_blocks = sets * p.mtiles, p.up_threads = 256;
+  return p;
+}
+
+// Whether both launches hold their threads.  (How many CUs there are decides about launches of a few workgroups
+// for each, far from this.)
+inline bool adapter_fits(const sc_adapter& a) {
+  if (a.B == 0 || a.L == 0) return true;
+  const AdapterPlan p = adapter_plan(a, 256);
+  return p.down_blocks * p.down_threads < kGridThreads && p.up_blocks * p.up_threads < kGridThreads;
+}
+
 }  // namespace sc

@@ -210,3 +210,25 @@ def test_scan_launches_fit_the_grid():
     for B, D, L, N, G in (((1 << 12) - 1, 1 << 12, 5, 4, 1 << 12), (1 << 16, (1 << 12) - 16, 2, 4, 1), ((1 << 24) - 1, 3, 7, 16, 1),
                           (1 << 16, 1 << 12, 1, 4, 1), (1 << 17, 1 << 13, 1, 30, 1), (1, (1 << 31) - 257, 1, 1, 1)):
         assert _status(sc.sparseconv_selective_scan, _far_scan(B, D, L, N, G)) == sc.SC_EDEVICE, (B, D, L, N, G)
+
+
+def test_adapter_launches_fit_the_grid():
+    """As for the scan: the documented limits, on both sides."""
+    import torch
+
+    def args(dtype, B, C, M, L, R=1):
+        return _adapter(dtype=dtype, B=B, C=C, M=M, L=L, R=R, adapters=1, x=1 << 44, base=0, out=2 << 44, down=3 << 44, up=4 << 44,
+                        scale=0, index=5 << 44, workspace=6 << 44, workspace_bytes=1 << 43, x_channel=L, x_batch=C * L, out_channel=L,
+                        out_batch=M * L)
+    for case in ((0, 1 << 23, 1, 1, 64), (0, 1 << 22, 1, 2, 65), (1, 1 << 23, 1, 1, 128), (2, 1 << 13, 1, 1, 1 << 17), (0, 1 << 23, 1, 1, 1),
+                 (1, 1 << 21, 1, 1000, 4), (1, 1 << 20, 1, 1025, 4), (0, 1, (1 << 31) - 1023, 1, 1), (1, 1, 1, (1 << 31) - 1023, 9),
+                 (0, (1 << 23), 1, 1, 40, 128)):
+        assert _status(sc.sparseconv_adapter_apply, args(*case)) == EUNSUPPORTED, case
+        with pytest.raises(sc.SparseConvError, match="SC_EUNSUPPORTED"):
+            sc.sparseconv_adapter_workspace(args(*case))
+    if torch.cuda.is_available():
+        return
+    for case in ((0, (1 << 23) - 1, 1, 1, 64), (0, (1 << 22) - 1, 1, 2, 65), (1, (1 << 23) - 1, 1, 1, 128), (2, (1 << 13) - 1, 1, 1, 1 << 17),
+                 (0, (1 << 23) - 1, 1, 1, 1), (1, (1 << 21) - 1, 1, 1000, 4), (0, 1, (1 << 31) - 1024, 1, 1), (1, 1, 1, (1 << 31) - 1024, 9),
+                 (0, (1 << 23) - 1, 1, 1, 40, 128), (1, 1, 1, 1000, (1 << 30) - 128)):
+        assert _status(sc.sparseconv_adapter_apply, args(*case)) == sc.SC_EDEVICE, case
