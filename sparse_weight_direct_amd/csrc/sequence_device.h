@@ -40,13 +40,14 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 
-// v * sigmoid(v).  exp2 and rcp are exact to 1 ulp, well inside what the fp32 sums before it carry.
+// v * sigmoid(v).  exp2 and rcp are exact to 1 ulp, well inside what the fp32 sums before it carry.  From v = -87.4
+// down the result is 0 (rcp makes no denormals): off by 1.3e-36 at most.
 __device__ __forceinline__ float silu(float v) {
   return v * __builtin_amdgcn_rcpf(1.0f + exp2_fast(-kLog2e * v));
 }
 
-// log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|), to 4.3 x 2^-24 of every result (measured over
-// -40..25): the small ones count (time steps of 1e-3).  With u = 1 + e rounded, e - (u - 1) is what the
+// log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|), to 4.7 x 2^-24 of every result (4 million values
+// over -40..25): the small ones count (time steps of 1e-3).  With u = 1 + e rounded, e - (u - 1) is what the
 // rounding lost, exactly, and log1p(e) = log(u) + that / u, where / u changes less than a rounding.
 // exp2's argument carries its rounding error along; |v| is bounded for that (e is 0 from 88 on), or the
 // product would be infinite at the ends of the range and the error no number: softplus(-inf) is 0 and
