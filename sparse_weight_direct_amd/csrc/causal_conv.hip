@@ -162,10 +162,7 @@ int launch_one(const sc_causal_conv& a, hipStream_t st) {
   }
   const int nv = (int)conv_places(a), blocks = (nv + 255) / 256;
   const int64_t rows = (int64_t)a.B * a.D;
-  // Rows that keep 4/5 (fp32: 2/3) of a workgroup busy get workgroups of their own (2048 positions, bf16: 29.4 instead of
-  // 30.4 us for 8 x 2048 rows, fp32 11.9 instead of 14.0 for 5 x 1000 of 1537); with less the idle threads cost
-  // more (2500 positions, bf16, 4 x 2048 rows: 27.2 instead of 20.8 us).
-  if (blocks * 256 * 4 <= (sizeof(T) == 4 ? 6 : 5) * nv)
+  if (conv_own_rows(a))
     hipLaunchKernelGGL((causal_conv_rows<T, K, SILU, true>), dim3((unsigned)(rows * blocks)), dim3(256), 0, st, a, blocks, nv);
   else
     hipLaunchKernelGGL((causal_conv_rows<T, K, SILU, false>), dim3((unsigned)((rows * nv + 255) / 256)), dim3(256), 0, st, a,

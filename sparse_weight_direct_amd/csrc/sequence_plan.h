@@ -24,6 +24,23 @@ inline int64_t conv_places(const sc_causal_conv& a) { return std::max<int64_t>(1
 // The limit on its sizes: fewer than 2^31 of them (workgroups that stay in a row add less than half).
 inline bool conv_fits(const sc_causal_conv& a) { return (int64_t)a.B * a.D < (1LL << 31) && (int64_t)a.B * a.D * conv_places(a) < (1LL << 31); }
 
+// Whether rows get workgroups of their own.  Measured, us, own workgroups / all places in one line, by the share of the
+// threads that own workgroups keep busy (six inputs in rotation, K = 4):
+//
+//   8 x 2048 rows     0.59        0.75        0.83        0.93        0.98        1.0
+//   bf16, 1 a row     21.3/18.6   30.5/25.4   28.0/25.7   28.4/27.9   26.2/26.0   26.0/26.2
+//   bf16, 2 a row     45.8/34.5   46.2/39.1   47.2/42.2   51.8/49.1   47.5/49.8   48.3/50.2
+//   fp32, 1 a row     38.3/38.9   42.7/45.4   49.0/48.9   53.5/53.8   53.3/52.3   53.3/52.4
+//   fp32, 2 a row                            102.2/83.9  101.3/99.2  100.8/97.2   99.1/98.7
+//
+// (nearest sizes: 0.61 and 0.71 for bf16 with 2 a row, 0.64 for fp32; 5 x 1000 rows in fp32: 13.1/13.8, 16.8/17.8,
+// 18.6/18.9, 20.4/21.0; 31.0/25.2 with 2 a row at 0.61.)  So 16-bit rows have to fill them, and fp32 gains where one
+// workgroup takes a row.
+inline bool conv_own_rows(const sc_causal_conv& a) {
+  const int64_t places = conv_places(a), threads = ceil_div(places, 256) * 256;
+  return a.dtype == SC_F32 ? threads == 256 && 3 * places >= 2 * threads : 32 * places >= 31 * threads;
+}
+
 // ---- Selective scan
 constexpr int kScanRows = 16;     // channels per workgroup of a prompt
 constexpr int kScanThreads = 256;
@@ -54,7 +71,8 @@ inline int64_t scan_token_channels(int N) { return 4 * (kScanThreads / scan_toke
 //   1 x 1024      16      14.3    10.8    24.6    22.0    24.3
 //                  8      13.4    12.4    19.4    17.2    27.9
 //
-// so eight up to 384 positions unless they fill a chunk of sixteens; above, the two change places with every chunk.
+// so eight up to 384 positions unless they fill a chunk of sixteens; above, the two change places with every chunk, and
+// sixteen is taken throughout (at 520, where two of three chunks are full, that costs 17% in the largest of these).
 struct ScanPlan {
   int ti, chunks, segments;  // positions per lane; chunks of 16 of them per segment
   int64_t groups;            // workgroups of a segment

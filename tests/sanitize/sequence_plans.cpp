@@ -1,5 +1,5 @@
 // Prints the plans that the sequence operators' launches take (sequence_plan.h) on a device of 256 CUs: one line a
-// call on standard input, "conv B D L", "scan B D L N G" or "adapter dtype B C M L R".
+// call on standard input, "conv dtype B D L", "scan B D L N G" or "adapter dtype B C M L R".
 #include <cstdio>
 #include <iostream>
 #include <string>
@@ -11,8 +11,8 @@ int main() {
   while (std::cin >> op) {
     if (op == "conv") {
       sc_causal_conv a{};
-      std::cin >> a.B >> a.D >> a.L;
-      std::printf("places=%lld fits=%d\n", (long long)sc::conv_places(a), sc::conv_fits(a));
+      std::cin >> a.dtype >> a.B >> a.D >> a.L;
+      std::printf("places=%lld own=%d fits=%d\n", (long long)sc::conv_places(a), sc::conv_own_rows(a), sc::conv_fits(a));
     } else if (op == "scan") {
       sc_selective_scan a{};
       std::cin >> a.B >> a.D >> a.L >> a.N >> a.G;

@@ -31,6 +31,14 @@ def _scan_forms(p):
     return {(p["ti"], False, bool(p["ahead"]))} | ({(p["ti"], True, bool(p["ahead"]))} if p["segments"] > 1 else set())
 
 
+def test_both_forms_of_the_convolution_are_tested(plans):
+    """test_conv_long_rows: 1700, 2041, 2048, 2049 and 4090 positions."""
+    lengths = (1700, 2041, 2048, 2049, 4090)
+    for dtype, own in ((0, [1, 1, 1, 0, 0]), (1, [0, 1, 1, 0, 1]), (2, [0, 1, 1, 0, 1])):
+        p = plans(*(("conv", dtype, 2, 3, L) for L in lengths))
+        assert [v["own"] for v in p] == own and [v["places"] for v in p] == [-(-L // 8) for L in lengths]
+
+
 def test_every_form_of_the_scan_is_tested(plans):
     sizes = [("scan", 2, 5, 64, 16, 1), ("scan", 2, 5, 300, 16, 1), ("scan", 2, 5, 1025, 16, 1), ("scan", 2, 19, 512, 16, 1),
              ("scan", 9, 1023, 520, 20, 1), ("scan", 9, 1023, 520, 16, 1), ("scan", 2, 512, 2311, 20, 1), ("scan", 1, 1024, 2500, 16, 4)]
@@ -88,7 +96,8 @@ def test_plans_cover_their_work(plans):
 def test_plans_at_the_ends(plans):
     """Under the sanitizer: no sum passes its type."""
     top = (1 << 31) - 1
-    conv = plans(("conv", 1, 1, top), ("conv", 7, 1, top), ("conv", 8, 1, top), ("conv", 1, top, 1), ("conv", top, top, top), ("conv", 1, 1, 0))
+    conv = plans(("conv", 1, 1, 1, top), ("conv", 0, 7, 1, top), ("conv", 1, 8, 1, top), ("conv", 2, 1, top, 1), ("conv", 0, top, top, top),
+                 ("conv", 0, 1, 1, 0))
     assert [p["fits"] for p in conv] == [1, 1, 0, 1, 0, 1] and conv[0]["places"] == 1 << 28 and conv[-1]["places"] == 1
     scan = plans(("scan", 1, top, 1, 1, 1), ("scan", 1, top, 1, 256, top), ("scan", top, 1, 1 << 29, 16, 1), ("scan", 1, 1, (1 << 30) - 1, 16, 1))
     assert [p["fits"] for p in scan] == [0, 0, 0, 1]
