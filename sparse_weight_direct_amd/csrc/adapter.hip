@@ -5,8 +5,8 @@
 // Bound by memory: x and base are read and out is written once; the R values a position between the two
 // products are a workspace that stays in L2 (R / (C + 2 M) of the rest).  Measured: fp32, 8 x 2048 -> 4096
 // channels x 1024 positions, R = 16: 72 us (16 and 56 for the two products), 4.7 TB/s, where a copy of 1 GiB
-// runs at 5.1; bf16, 12 x 1001 -> 1500 x 333, R = 24: 18.7 us (7 and 12), two launches of which most is
-// latency.  64 single positions of 4096 -> 4096 channels, 32 adapters, bf16: 8.2 us in one launch.
+// runs at 5.1; bf16, 12 x 1001 -> 1500 x 333, R = 24: 19.0 us (7 and 12): each of a tile's 12
+// workgroups of the second product reads all R values of the four pieces of C again, 64 KB from L2.  64 single positions of 4096 -> 4096 channels, 32 adapters, bf16: 8.2 us in one launch.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

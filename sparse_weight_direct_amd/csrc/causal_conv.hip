@@ -3,10 +3,9 @@
 //   out[b,d,t] = act(bias[d] + sum_k w[d,k] u[b,d,t-K+1+k]),  u = the initial state, then x.
 //
 // Bound by memory: every input is read and every output written once, 2 K + 10 instructions a value.
-// Measured (bf16, K = 4): 8 x 2048 rows of 2048 positions 28.6 us, 4.7 TB/s of x and out, where a copy of
+// Measured (bf16, K = 4): 8 x 2048 rows of 2048 positions 28.2 us, 4.8 TB/s of x and out, where a copy of
 // 1 GiB runs at 5.1; 4 x 2048 rows in fp32 at 5.8 TB/s.  Two or four rows a thread in flight were slower
-// (30.3 and 32.1 us), as was one place per thread in long rows (30.4).  Single positions: 128 x 4096
-// channels 4.4 us, a launch.
+// (30.3 and 32.1 us).  Single positions: 128 x 4096 channels 4.4 us, a launch.
 #include <hip/hip_runtime.h>
 
 #include "sequence_device.h"

@@ -5,10 +5,10 @@
 // Prompts are bound by vector issue: a state and position costs 1 exp2 (8 cycles a wavefront), 2 products
 // and 3 FMAs (4 each), 28 cycles, and there is nothing here that the matrix cores could take: the decay
 // differs per channel, state and position.  4 x 4096 channels x 2048 positions x 16 states (bf16): 96 us
-// of that alone at 2.4 GHz, 50 us of memory traffic, measured 165 us with the vector units busy 88 to 91% of
-// the time; the rest of the instructions are softplus, gate and conversions (34 a position, shared by 16 states),
+// of that alone at 2.4 GHz, 50 us of memory traffic, measured 166 us with the vector units busy 88% of
+// the time; the rest of the instructions are softplus, gate and conversions (36 a position, shared by 16 states),
 // the lanes' scan (22 a state, shared by 16 positions) and the staging of b and c.
-// Single positions are bound by the states' bytes: 128 x 4096 channels x 16 states 15.3 us, 4.7 TB/s.
+// Single positions are bound by the states' bytes: 128 x 4096 channels x 16 states 15.4 us, 4.6 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
