@@ -517,6 +517,148 @@ sc_status sparseconv_adapter_apply(const sc_adapter* a, void* hip_stream);
  * looked at.  Errors as sparseconv_selective_scan_workspace. */
 sc_status sparseconv_adapter_workspace(const sc_adapter* a, int64_t* bytes);
 
+/*
+ * ---- Attention operators ----------------------------------------------------------------
+ *
+ * What a pruned sequence model needs beside the operators above where its layers attend: attention
+ * of new positions over a paged cache, rotary positions with the cache's update, copies of pages,
+ * and the norms around a block with its residual sum.  Conventions are the sequence operators'
+ * (tensors (B, channels, L) with free batch and channel strides, fp32 sums, one rounding, lengths,
+ * asynchronous, no allocation, capturable), and:
+ *  - A cache has `pages` pages of P positions (16, 32, 64, 128 or 256) for each of its G heads of D dims: keys
+ *    as G x P x D values a page, values as G x D x P (positions contiguous, so that both products read
+ *    whole 16 bytes), pages k_page and v_page values apart.  Both are 16-byte aligned, and so are
+ *    their pages; D is a multiple of 8, at most 256.
+ *  - Position t of sequence b is at place t % P of page table[b*table_batch + t / P], t / P < width.  An
+ *    entry outside 0 .. pages-1 is no page: nothing is written to it, and nobody sees what it would hold.
+ *    Pages may be shared between sequences that only read them; a page that a call writes must be one
+ *    sequence's alone.
+ *  - past[b]: positions of sequence b before this call's, so the call's position i is the sequence's
+ *    past[b] + i.  A sequence whose past is outside 0 .. width*P is idle: its outputs are 0
+ *    and nothing of it is written.  width*P <= 2^30.
+ */
+
+#define SC_ATT_OUT_F32 1u     /* attention: out is fp32 whatever the dtype */
+#define SC_ROT_INTERLEAVED 1u /* append: a pair is dims 2j, 2j+1 instead of j, j + pairs */
+
+typedef struct {
+  const void* q;          /* device, (B, H*D, L): head h has channels h*D .. h*D+D-1 */
+  void* out;              /* device, (B, H*D, L) */
+  const void* k_pages;    /* device, of type dtype */
+  const void* v_pages;    /* device, of type dtype */
+  const int32_t* table;   /* device, B x width */
+  const int32_t* past;    /* device, B */
+  const int32_t* lengths; /* device, B; NULL: L */
+  const int32_t* prefix;  /* device, B; NULL: none */
+  const float* slopes;    /* device, H; NULL: none */
+  void* workspace;        /* device, 16-byte aligned, sparseconv_paged_attention_workspace bytes */
+  int64_t workspace_bytes;
+  int64_t q_batch, q_channel, out_batch, out_channel; /* strides */
+  int64_t k_page, v_page;                             /* between pages */
+  int64_t table_batch;
+  float scale, cap;                                   /* cap 0: none */
+  int32_t dtype, B, H, G, D, L, P, width, pages;      /* G divides H */
+  int32_t window;                                     /* 0: none */
+  uint32_t flags;                                     /* 0 or SC_ATT_OUT_F32 */
+  int32_t reserved;                                   /* 0 */
+} sc_paged_attention;
+
+/*
+ * Attention of L new positions a sequence over the cache, which holds them already (append first):
+ *     out[b,h,i] = sum_t p_t v_t / sum_t p_t,  p_t = exp(s_t),
+ *     s_t = f(scale q[b,h,i] . k_t) - slopes[h] |past + i - t|,  f(s) = cap tanh(s / cap) with a cap
+ * over the visible positions t < past[b] + lengths[b] of head h / (H/G): those with t < prefix[b], and
+ * those with t <= past + i and, with a window, past + i - t < window.  (So a prefix is seen whole by
+ * every position, also from within it and from beyond the window.)  Where nothing is visible out is 0.
+ * What is not visible may hold anything, infinities and NaN included.  Sums and softmax in fp32; the weights
+ * p are rounded to dtype for the second product (relative to the row's largest score so far), which is a choice: an output
+ * is off by up to half a unit of dtype of its terms' magnitudes beside its own rounding.
+ * B, L >= 0.  Limits: L < 2^30, H, G <= 2^16, and fewer than 2^24 workgroups: B*G*ceil(H/G*L/16) < 2^24
+ * with L rounded up to a multiple of 128 from there on.
+ */
+sc_status sparseconv_paged_attention(const sc_paged_attention* a, void* hip_stream);
+
+/* Device workspace such a call needs, in bytes (0 if none).  Only the sizes of *a are looked at.
+ * Errors: SC_EINVAL (NULL), SC_ESHAPE, SC_EUNSUPPORTED. */
+sc_status sparseconv_paged_attention_workspace(const sc_paged_attention* a, int64_t* bytes);
+
+typedef struct {
+  const void* q;            /* device, (B, H*D, L); NULL: keys and values alone */
+  void* q_out;              /* device, (B, H*D, L) of the cache's type; may be q itself where the types are the same */
+  const void* k;            /* device, (B, G*D, L) */
+  const void* v;            /* device, (B, G*D, L) */
+  void* k_pages;            /* device, of type cache_dtype */
+  void* v_pages;            /* device, of type cache_dtype */
+  const double* freqs;      /* device, `pairs` angles a position, in radians; NULL: no rotation (pairs 0) */
+  const int32_t* axes;      /* device, `pairs`: the coordinate that turns each pair; NULL: 0 */
+  const int32_t* positions; /* device, (B, num_axes, L); NULL: past + i */
+  const int32_t* table;     /* device, B x width */
+  const int32_t* past;      /* device, B */
+  const int32_t* lengths;   /* device, B; NULL: L */
+  int64_t q_batch, q_channel, q_out_batch, q_out_channel, k_batch, k_channel, v_batch, v_channel;
+  int64_t k_page, v_page, table_batch, positions_batch, positions_axis;
+  int32_t dtype, cache_dtype, B, H, G, D, L, P, width, pages; /* cache_dtype: dtype, or with SC_F32 any */
+  int32_t pairs, num_axes;                                    /* 2*pairs <= D; num_axes >= 1 */
+  uint32_t flags;                                             /* 0 or SC_ROT_INTERLEAVED */
+  int32_t reserved;                                           /* 0 */
+} sc_cache_append;
+
+/*
+ * Turns the pairs (x_j, x_{j+pairs}) of the first 2*pairs dims of every head of q and k by
+ * freqs[j] * positions[b, axes[j], i] (a pair whose axis is outside 0 .. num_axes-1 stays), and writes k and
+ * v of the new positions into the cache; q goes to q_out, 0 past a sequence's length.  Angles are
+ * reduced in fp64, so far positions are as exact as near ones.  Positions at or past width*P, or on no page, are not
+ * written.  B, L >= 0.  Limits: L < 2^30, H, G <= 2^16, and with W = H + 2 G (2 G without q) B*W*D*L < 2^32 where L < 16, else
+ * B*(ceil(L/64) + 1)*(ceil(W/8) + 1) < 2^24.
+ */
+sc_status sparseconv_cache_append(const sc_cache_append* a, void* hip_stream);
+
+typedef struct {
+  void* pool;            /* device: `outer` blocks (layers, keys and values) of `pages` pages */
+  const int32_t* source; /* device, count */
+  const int32_t* target; /* device, count */
+  int64_t outer_stride, page_stride, page_bytes; /* bytes */
+  int32_t outer, pages, count, reserved;         /* reserved 0 */
+} sc_cache_copy;
+
+/*
+ * Copies page source[i] over page target[i] in every block, i < count.  A pair with an entry outside
+ * 0 .. pages-1 is left out.  No page may be the target of two pairs, or of one and the source of another: the order of the
+ * copies is not defined.  16 bytes at a time where the pool, its strides and its pages are multiples
+ * of 16, else one.  Limits: fewer than 2^24 workgroups, outer*count*ceil(page_bytes/16384).
+ */
+sc_status sparseconv_cache_copy(const sc_cache_copy* a, void* hip_stream);
+
+#define SC_NORM_CENTER 1u /* both norms subtract the mean */
+
+typedef struct {
+  const void* x;            /* device, (B, C, L): the residual stream */
+  const void* y;            /* device, (B, C, L): the block's output; NULL: none */
+  const void* gate;         /* device, (B, C, L); NULL: none */
+  void* sum;                /* device, (B, C, L): the new residual stream; NULL: not wanted.  May be x itself */
+  void* out;                /* device, (B, C, L): its norm; NULL: not wanted.  May be y itself */
+  const float* weight;      /* device, C: of the norm that makes out; NULL: 1 */
+  const float* bias;        /* device, C; NULL: 0 */
+  const float* post_weight; /* device, C: norm of y; NULL: y as it is */
+  const float* post_bias;   /* device, C; NULL: 0 */
+  int64_t x_batch, x_channel, y_batch, y_channel, sum_batch, sum_channel, out_batch, out_channel;
+  int64_t gate_batch, gate_channel, gate_position; /* gate_position 0 or 1 */
+  float scale, eps;
+  int32_t dtype, B, C, L;
+  uint32_t flags;                                  /* 0 or SC_NORM_CENTER */
+  int32_t reserved;                                /* 0 */
+} sc_residual_norm;
+
+/*
+ * The norms around a block, over the channels of each position:
+ *     r = x + scale * gate * post(y),  sum = r,  out = norm(r) * weight + bias,
+ *     norm(v) = (v - m) / sqrt(mean((v - m)^2) + eps),  m = mean(v) with SC_NORM_CENTER, else 0,
+ *     post(v) = norm(v) * post_weight + post_bias where there is a post_weight, else v.
+ * r is normed before it is rounded.  "x itself": the same pointer and strides.  B, L >= 0, C >= 1.
+ * Limits: C < 2^20, L < 2^30, B*ceil(L/8) < 2^22.
+ */
+sc_status sparseconv_residual_norm(const sc_residual_norm* a, void* hip_stream);
+
 /* Message of the calling thread's last failure ("" if none).  Valid until that thread's
  * next call into the library. */
 const char* sparseconv_last_error(void);

@@ -9,8 +9,8 @@ The functions keep the C names:
     sparseconv_pack, sparseconv_forward, sparseconv_forward_workspace,
     sparseconv_workspace_size, sparseconv_query, sparseconv_export_packed,
     sparseconv_export_words, sparseconv_destroy, sparseconv_last_error
-plus ``Handle`` (owns a packed filter bank and destroys it when collected) and the sequence
-operators (sequence.py; a pruned layer that uses them: ssm.py).  The dense direct baseline is a Handle packed with SC_PACK_ALL_TAPS (every filter tap stored).
+plus ``Handle`` (owns a packed filter bank and destroys it when collected), the sequence
+operators (sequence.py; a pruned layer that uses them: ssm.py) and the attention operators (attention.py).  The dense direct baseline is a Handle packed with SC_PACK_ALL_TAPS (every filter tap stored).
 """
 from __future__ import annotations
 
@@ -49,7 +49,9 @@ EXPORTED = ("sparseconv_pack", "sparseconv_forward", "sparseconv_forward_workspa
             "sparseconv_export_kernel_source", "sparseconv_launch_info", "sparseconv_device_status",
             "sparseconv_dense_forward", "sparseconv_forward_noalloc", "sparseconv_tune", "sparseconv_destroy",
             "sparseconv_causal_conv", "sparseconv_selective_scan", "sparseconv_selective_scan_workspace",
-            "sparseconv_adapter_apply", "sparseconv_adapter_workspace", "sparseconv_last_error")
+            "sparseconv_adapter_apply", "sparseconv_adapter_workspace", "sparseconv_paged_attention",
+            "sparseconv_paged_attention_workspace", "sparseconv_cache_append", "sparseconv_cache_copy",
+            "sparseconv_residual_norm", "sparseconv_last_error")
 
 
 class sc_weights(ctypes.Structure):
@@ -404,3 +406,7 @@ class Handle:
 from .sequence import (adapter_apply, causal_conv, causal_conv_step, selective_scan, selective_scan_step,  # noqa: E402,F401
                        selective_scan_workspace, sparseconv_adapter_apply, sparseconv_adapter_workspace,
                        sparseconv_causal_conv, sparseconv_selective_scan, sparseconv_selective_scan_workspace)
+from .attention import (cache_append, cache_append_step, cache_copy, paged_attention, paged_attention_step,  # noqa: E402,F401
+                        paged_attention_workspace, residual_norm, residual_norm_step, sparseconv_cache_append,
+                        sparseconv_cache_copy, sparseconv_paged_attention, sparseconv_paged_attention_workspace,
+                        sparseconv_residual_norm)

@@ -10,8 +10,9 @@ LIB = os.path.join(HERE, "libsparseconv.so")
 PROBE_LIB = os.path.join(HERE, "libscprobe.so")  # roof probes timed by the benchmark
 PROBE_SOURCE = os.path.join(HERE, "csrc", "probes.hip")
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("kernels.hip", "escoin.hip", "dense.hip", "pack.cpp", "bake.cpp", "api.cpp",
-                                               "causal_conv.hip", "selective_scan.hip", "adapter.hip", "sequence.cpp")]
-BINDING_LIB = os.path.join(HERE, "_binding.so")  # tensor arguments of the sequence operators
+                                               "causal_conv.hip", "selective_scan.hip", "adapter.hip", "sequence.cpp",
+                                               "paged_attention.hip", "cache.hip", "residual_norm.hip", "attention.cpp")]
+BINDING_LIB = os.path.join(HERE, "_binding.so")  # tensor arguments of the sequence and attention operators
 BINDING_SOURCE = os.path.join(HERE, "csrc", "binding.cpp")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -1,4 +1,4 @@
-// Tensor arguments of the sequence operators: checks each torch tensor's type, device, shape and
+// Tensor arguments of the sequence and attention operators: checks each torch tensor's type, device, shape and
 // strides, allocates what the caller has not given, fills the C ABI's argument structure and calls it.
 // Marshalling only, like the ctypes part of the package; it is native because the single-token calls
 // take 4 us on the GPU, and the same checks in Python took 5 us of host time beside the launch's 3.7.
@@ -16,8 +16,10 @@
 #include <c10/core/GradMode.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <sstream>
 #include <stdexcept>
+#include <vector>
 
 #include "../../include/sparseconv.h"
 
@@ -246,6 +248,268 @@ PyObject* adapter_apply(PyObject* const* v, Py_ssize_t n) {
   return answer(sparseconv_adapter_apply(&a, PyLong_AsVoidPtr(v[8])), out, v[6], Py_None);
 }
 
+double number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) {
+    PyErr_Clear();
+    refuse("scale, cap and eps must be numbers");
+  }
+  return v;
+}
+
+// Both halves of a cache: k_pages (pages, G, P, D) and v_pages (pages, G, D, P), each page contiguous.
+struct Pages {
+  const Tensor &k, &v;
+  int64_t pages, G, P, D;
+
+  Pages(const Call& c, PyObject* ko, PyObject* vo, at::ScalarType type) : k(tensor(ko, "k_pages")), v(tensor(vo, "v_pages")) {
+    if (k.dim() != 4 || v.dim() != 4) refuse("k_pages must be (pages, heads, positions, dims) and v_pages (pages, heads, dims, positions)");
+    pages = k.size(0), G = k.size(1), P = k.size(2), D = k.size(3);
+    check(c, k, "k_pages", type, {pages, G, P, D});
+    check(c, v, "v_pages", type, {pages, G, D, P});
+  }
+  static void check(const Call& c, const Tensor& t, const char* name, at::ScalarType type, Shape shape) {
+    int64_t per = 1;
+    bool dense = true;
+    for (int i = 3; i >= 1; i--) {
+      if (shape[i] > 1 && t.stride(i) != per) dense = false;
+      per *= shape[i];
+    }
+    if (!c.fits(t, type, shape) || !dense) refuse_tensor(t, name, type, shape, "each page contiguous");
+  }
+  int64_t stride(const Tensor& t) const { return pages > 1 ? t.stride(0) : G * P * D; }
+};
+
+// table (B, width): its rows may be part of a wider one.
+const int32_t* table_of(const Call& c, PyObject* o, int64_t B, int64_t* width, int64_t* batch) {
+  const Tensor& t = tensor(o, "table");
+  *width = t.dim() == 2 ? t.size(1) : 0;
+  const int64_t shape[2] = {B, *width};
+  if (t.dim() != 2 || !c.fits(t, at::kInt, shape) || (*width > 1 && t.stride(1) != 1)) refuse_tensor(t, "table", at::kInt, shape, "its rows contiguous");
+  *batch = B > 1 ? t.stride(0) : *width;
+  return static_cast<const int32_t*>(t.data_ptr());
+}
+
+// q, k_pages, v_pages, table, past, lengths, prefix, slopes, scale, cap, window, out, workspace, axes of q, stream
+PyObject* paged_attention(PyObject* const* v, Py_ssize_t n) {
+  check(n, 15);
+  const Call c(tensor(v[0], "q"));
+  const Tensor& q = c.x;
+  const int64_t axes = PyLong_AsLong(v[13]);
+  const bool chunk = axes == 3;
+  if (q.dim() != axes) refuse(chunk ? "q must be (B, H*D, L)" : "q must be (B, H*D)");
+  const Pages pages(c, v[1], v[2], c.type);
+  const c10::DeviceGuard guard(c.device);
+  const int64_t B = q.size(0), D = pages.D, G = pages.G, L = chunk ? q.size(2) : 1;
+  if (D == 0 || q.size(1) % D) refuse("q's channels are no multiple of the cache's dims");
+  const int64_t H = q.size(1) / D;
+  c.activation(q, "q", q.sizes(), chunk);
+  sc_paged_attention a{};
+  int64_t width;
+  a.table = table_of(c, v[3], B, &width, &a.table_batch);
+  a.past = c.dense<int32_t>(v[4], "past", at::kInt, {B});
+  a.lengths = c.dense<int32_t>(v[5], "lengths", at::kInt, {B});
+  a.prefix = c.dense<int32_t>(v[6], "prefix", at::kInt, {B});
+  a.slopes = c.dense<float>(v[7], "slopes", at::kFloat, {H});
+  a.scale = v[8] == Py_None ? (float)(1.0 / std::sqrt((double)D)) : (float)number(v[8]);
+  a.cap = (float)number(v[9]);
+  const long long window = PyLong_AsLongLong(v[10]);
+  if (window == -1 && PyErr_Occurred()) return nullptr;
+  if (window < 0) refuse("window must be 0 (none) or positive");
+  Tensor out;
+  if (v[11] == Py_None) {
+    out = at::empty(q.sizes(), q.options());
+  } else {
+    out = tensor(v[11], "out");
+    if (out.scalar_type() == at::kFloat && c.type != at::kFloat) {
+      a.flags = SC_ATT_OUT_F32;
+      if (!c.fits(out, at::kFloat, q.sizes()) || (chunk && L > 1 && out.stride(-1) != 1))
+        refuse_tensor(out, "out", at::kFloat, q.sizes(), chunk ? "its last axis contiguous" : "strided");
+    } else {
+      c.activation(out, "out", q.sizes(), chunk);
+    }
+  }
+  a.q = q.data_ptr(), a.out = out.data_ptr(), a.k_pages = pages.k.data_ptr(), a.v_pages = pages.v.data_ptr();
+  a.q_batch = q.stride(0), a.q_channel = q.stride(1), a.out_batch = out.stride(0), a.out_channel = out.stride(1);
+  a.k_page = pages.stride(pages.k), a.v_page = pages.stride(pages.v);
+  a.dtype = c.dtype(), a.B = c.size(B), a.H = c.size(H), a.G = c.size(G), a.D = c.size(D), a.L = c.size(L), a.P = c.size(pages.P);
+  a.width = c.size(width), a.pages = c.size(pages.pages);
+  a.window = window > INT32_MAX ? 0 : (int32_t)window;  // positions end below 2^31
+  int64_t need = 0;
+  if (const sc_status s = sparseconv_paged_attention_workspace(&a, &need)) return PyLong_FromLong(s);
+  const Tensor ws = c.workspace(v[12], need);
+  if (need) a.workspace = ws.data_ptr(), a.workspace_bytes = (int64_t)ws.nbytes();
+  return answer(sparseconv_paged_attention(&a, PyLong_AsVoidPtr(v[14])), out, v[11], Py_None);
+}
+
+// k, v, k_pages, v_pages, table, past, q, freqs, axes, positions, interleaved, lengths, out, axes of k, stream
+PyObject* cache_append(PyObject* const* v, Py_ssize_t n) {
+  check(n, 15);
+  const Call c(tensor(v[0], "k"));
+  const Tensor &k = c.x, &val = tensor(v[1], "v");
+  const int64_t axes = PyLong_AsLong(v[13]);
+  const bool chunk = axes == 3;
+  if (k.dim() != axes) refuse(chunk ? "k must be (B, G*D, L)" : "k must be (B, G*D)");
+  const at::ScalarType cache = tensor(v[2], "k_pages").scalar_type();
+  if (cache != c.type && !(c.type == at::kFloat && (cache == at::kBFloat16 || cache == at::kHalf)))
+    refuse("k_pages must be of k's type, or narrower than a float32 k");
+  const Pages pages(c, v[2], v[3], cache);
+  const c10::DeviceGuard guard(c.device);
+  const int64_t B = k.size(0), G = pages.G, D = pages.D, L = chunk ? k.size(2) : 1;
+  std::vector<int64_t> shape = {B, G * D};
+  if (chunk) shape.push_back(L);
+  c.activation(k, "k", shape, chunk);
+  c.activation(val, "v", shape, chunk);
+  sc_cache_append a{};
+  int64_t width;
+  a.table = table_of(c, v[4], B, &width, &a.table_batch);
+  a.past = c.dense<int32_t>(v[5], "past", at::kInt, {B});
+  a.lengths = c.dense<int32_t>(v[11], "lengths", at::kInt, {B});
+  a.num_axes = 1;
+  if (v[7] != Py_None) {
+    const Tensor& freqs = tensor(v[7], "freqs");
+    const int64_t pairs = freqs.dim() == 1 ? freqs.size(0) : 0;
+    a.freqs = c.dense<double>(v[7], "freqs", at::kDouble, {pairs});
+    a.axes = c.dense<int32_t>(v[8], "axes", at::kInt, {pairs});
+    a.pairs = c.size(pairs);
+    if (v[9] != Py_None) {
+      const Tensor& p = tensor(v[9], "positions");
+      const int64_t want[3] = {B, p.dim() == 3 ? p.size(1) : 0, L};
+      if (p.dim() != 3 || want[1] < 1 || !c.fits(p, at::kInt, want) || (L > 1 && p.stride(2) != 1))
+        refuse_tensor(p, "positions", at::kInt, want, "its last axis contiguous, (B, axes, L)");
+      a.positions = static_cast<const int32_t*>(p.data_ptr());
+      a.positions_batch = p.stride(0), a.positions_axis = p.stride(1), a.num_axes = c.size(want[1]);
+    }
+  } else if (v[8] != Py_None || v[9] != Py_None) {
+    refuse("axes and positions need freqs");
+  }
+  a.flags = PyObject_IsTrue(v[10]) ? SC_ROT_INTERLEAVED : 0;
+  Tensor out;
+  if (v[6] != Py_None) {
+    const Tensor& q = tensor(v[6], "q");
+    if (q.dim() != axes || D == 0 || q.size(1) % D) refuse(chunk ? "q must be (B, H*D, L)" : "q must be (B, H*D)");
+    std::vector<int64_t> qs = {B, q.size(1)};
+    if (chunk) qs.push_back(L);
+    c.activation(q, "q", qs, chunk);
+    if (v[12] == Py_None) {
+      out = at::empty(qs, k.options().dtype(cache));
+    } else {
+      out = tensor(v[12], "out");
+      if (!c.fits(out, cache, qs) || (chunk && L > 1 && out.stride(-1) != 1))
+        refuse_tensor(out, "out", cache, qs, chunk ? "its last axis contiguous" : "strided");
+    }
+    a.q = q.data_ptr(), a.q_out = out.data_ptr(), a.H = c.size(q.size(1) / D);
+    a.q_batch = q.stride(0), a.q_channel = q.stride(1), a.q_out_batch = out.stride(0), a.q_out_channel = out.stride(1);
+    if (q.size(1) == 0) refuse("q has no heads");
+  } else if (v[12] != Py_None) {
+    refuse("out without q");
+  }
+  a.k = k.data_ptr(), a.v = val.data_ptr(), a.k_pages = pages.k.data_ptr(), a.v_pages = pages.v.data_ptr();
+  a.k_batch = k.stride(0), a.k_channel = k.stride(1), a.v_batch = val.stride(0), a.v_channel = val.stride(1);
+  a.k_page = pages.stride(pages.k), a.v_page = pages.stride(pages.v);
+  a.dtype = c.dtype(), a.cache_dtype = cache == at::kFloat ? SC_F32 : cache == at::kBFloat16 ? SC_BF16 : SC_F16;
+  a.B = c.size(B), a.G = c.size(G), a.D = c.size(D), a.L = c.size(L), a.P = c.size(pages.P), a.width = c.size(width), a.pages = c.size(pages.pages);
+  if (const sc_status s = sparseconv_cache_append(&a, PyLong_AsVoidPtr(v[14]))) return PyLong_FromLong(s);
+  written(v[2]);
+  written(v[3]);
+  written(v[12]);
+  if (v[6] == Py_None) Py_RETURN_NONE;
+  return THPVariable_Wrap(out);
+}
+
+// pool, source, target, stream
+PyObject* cache_copy(PyObject* const* v, Py_ssize_t n) {
+  check(n, 4);
+  const Tensor& pool = tensor(v[0], "pool");
+  if (!pool.is_cuda() || pool.dim() < 3) refuse("pool must be a tensor (outer, pages, ...) on the GPU");
+  int64_t per = 1;
+  for (int64_t i = pool.dim() - 1; i >= 2; i--) {
+    if (pool.size(i) > 1 && pool.stride(i) != per) refuse("each of pool's pages must be contiguous");
+    per *= pool.size(i);
+  }
+  const c10::DeviceGuard guard(pool.device());
+  sc_cache_copy a{};
+  const Tensor* which[2] = {&tensor(v[1], "source"), &tensor(v[2], "target")};
+  const int64_t count = which[0]->dim() == 1 ? which[0]->size(0) : 0, es = (int64_t)pool.element_size();
+  for (int i = 0; i < 2; i++) {
+    const Tensor& t = *which[i];
+    if (t.scalar_type() != at::kInt || t.device() != pool.device() || t.dim() != 1 || t.size(0) != count || !t.is_contiguous())
+      refuse_tensor(t, i ? "target" : "source", at::kInt, {count}, "contiguous");
+  }
+  a.pool = pool.data_ptr();
+  a.source = static_cast<const int32_t*>(which[0]->data_ptr()), a.target = static_cast<const int32_t*>(which[1]->data_ptr());
+  a.outer = Call::size(pool.size(0)), a.pages = Call::size(pool.size(1)), a.count = Call::size(count);
+  a.page_bytes = per * es;
+  a.page_stride = pool.size(1) > 1 ? pool.stride(1) * es : a.page_bytes;
+  a.outer_stride = pool.size(0) > 1 ? pool.stride(0) * es : a.page_stride * pool.size(1);
+  return answer(sparseconv_cache_copy(&a, PyLong_AsVoidPtr(v[3])), pool, v[0], Py_None);
+}
+
+// x, y, weight, bias, post_weight, post_bias, gate, scale, eps, center, sum, out, axes of x, stream
+PyObject* residual_norm(PyObject* const* v, Py_ssize_t n) {
+  check(n, 14);
+  const Call c(tensor(v[0], "x"));
+  const Tensor& x = c.x;
+  const int64_t axes = PyLong_AsLong(v[12]);
+  const bool chunk = axes == 3;
+  if (x.dim() != axes) refuse(chunk ? "x must be (B, C, L)" : "x must be (B, C)");
+  const c10::DeviceGuard guard(c.device);
+  const int64_t B = x.size(0), C = x.size(1), L = chunk ? x.size(2) : 1;
+  c.activation(x, "x", x.sizes(), chunk);
+  sc_residual_norm a{};
+  a.weight = c.dense<float>(v[2], "weight", at::kFloat, {C});
+  a.bias = c.dense<float>(v[3], "bias", at::kFloat, {C});
+  a.post_weight = c.dense<float>(v[4], "post_weight", at::kFloat, {C});
+  a.post_bias = c.dense<float>(v[5], "post_bias", at::kFloat, {C});
+  if (v[1] != Py_None) {
+    const Tensor& y = tensor(v[1], "y");
+    c.activation(y, "y", x.sizes(), chunk);
+    a.y = y.data_ptr(), a.y_batch = y.stride(0), a.y_channel = y.stride(1);
+  }
+  if (v[6] != Py_None) {
+    const Tensor& g = tensor(v[6], "gate");
+    const int64_t two[2] = {B, C};
+    if (g.dim() == 2) {
+      c.activation(g, "gate", two, false);
+    } else {
+      c.activation(g, "gate", x.sizes(), chunk);
+      a.gate_position = L > 1 ? 1 : 0;
+    }
+    a.gate = g.data_ptr(), a.gate_batch = g.stride(0), a.gate_channel = g.stride(1);
+  }
+  a.scale = (float)number(v[7]), a.eps = (float)number(v[8]);
+  a.flags = PyObject_IsTrue(v[9]) ? SC_NORM_CENTER : 0;
+  Tensor sum, out;
+  if (v[1] != Py_None || v[10] != Py_None) {  // without y the sum is x
+    sum = c.output(v[10], x.sizes(), chunk);
+    a.sum = sum.data_ptr(), a.sum_batch = sum.stride(0), a.sum_channel = sum.stride(1);
+  }
+  if (a.weight || v[11] != Py_None) {
+    if (v[11] == Py_None) {
+      out = at::empty(x.sizes(), x.options());
+    } else {
+      out = tensor(v[11], "out");
+      c.activation(out, "out", x.sizes(), chunk);
+    }
+    a.out = out.data_ptr(), a.out_batch = out.stride(0), a.out_channel = out.stride(1);
+  }
+  a.x = x.data_ptr(), a.x_batch = x.stride(0), a.x_channel = x.stride(1);
+  a.dtype = c.dtype(), a.B = c.size(B), a.C = c.size(C), a.L = c.size(L);
+  if (const sc_status s = sparseconv_residual_norm(&a, PyLong_AsVoidPtr(v[13]))) return PyLong_FromLong(s);
+  written(v[10]);
+  written(v[11]);
+  PyObject* r = PyTuple_New(2);
+  if (!r) return nullptr;
+  auto item = [](const Tensor& t) {
+    if (t.defined()) return THPVariable_Wrap(t);
+    Py_INCREF(Py_None);
+    return Py_None;
+  };
+  PyTuple_SET_ITEM(r, 0, sum.defined() ? item(sum) : item(x));
+  PyTuple_SET_ITEM(r, 1, item(out));
+  return r;
+}
+
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* entry(PyObject*, PyObject* const* v, Py_ssize_t n) {
   try {
@@ -269,7 +533,9 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef methods[] = {method<causal_conv>("causal_conv"), method<selective_scan>("selective_scan"),
-                         method<adapter_apply>("adapter_apply"), {nullptr, nullptr, 0, nullptr}};
+                         method<adapter_apply>("adapter_apply"), method<paged_attention>("paged_attention"),
+                         method<cache_append>("cache_append"), method<cache_copy>("cache_copy"),
+                         method<residual_norm>("residual_norm"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
