@@ -12,24 +12,28 @@ namespace sc {
 constexpr int64_t kMostGroups = 1LL << 24;  // workgroups of 256 threads that a launch holds
 
 // ---- Attention.  The rows of a head of keys are its H/G heads' positions, `pitch` apart from head to head; a
-// workgroup takes 16 * nt of them.
+// workgroup takes 16 * nt of them, or 64 * nt where its wavefronts share the keys.
 struct AttendPlan {
-  int nt;            // tiles of 16 rows
-  int pitch;         // rows a head: L, or L rounded up so that no tile has two heads
-  int64_t tiles;     // of one head of keys
+  bool staged;
+  int nt;            // tiles of 16 rows of a wavefront
+  int pitch;         // rows a head: L, or L rounded up so that no workgroup has two heads
+  int64_t tiles;     // workgroups of one head of keys
   int splits;        // pieces of the context
+  int rows() const { return (staged ? 64 : 16) * nt; }
   int64_t groups() const { return tiles * splits; }
 };
 
 // Tiles of rows whose queries and sums leave a wavefront's registers room for a block's keys and values.
 constexpr int attend_most_tiles(int64_t size, int dims) { return size * dims <= 256 ? 4 : size * dims <= 512 ? 2 : 1; }
+constexpr int attend_staged_tiles(int64_t size, int dims) { return size * dims <= 512 ? 2 : 1; }
 
 inline AttendPlan attend_plan(const sc_paged_attention& a, int cus) {
   AttendPlan p;
-  const int64_t share = a.H / a.G, rows = share * a.L;
-  const int most = attend_most_tiles(a.dtype == SC_F32 ? 4 : 2, a.D <= 64 ? 64 : a.D <= 128 ? 128 : 256);
-  p.nt = std::min(most, rows <= 16 ? 1 : rows <= 32 ? 2 : 4);
-  const int tile = 16 * p.nt;
+  const int64_t share = a.H / a.G, rows = share * a.L, size = a.dtype == SC_F32 ? 4 : 2;
+  const int dims = a.D <= 64 ? 64 : a.D <= 128 ? 128 : 256;
+  p.staged = rows >= 128;
+  p.nt = p.staged ? attend_staged_tiles(size, dims) : std::min(attend_most_tiles(size, dims), rows <= 16 ? 1 : rows <= 32 ? 2 : 4);
+  const int tile = p.rows();
   p.pitch = a.L < tile ? a.L : (int)(ceil_div(a.L, tile) * tile);
   p.tiles = ceil_div(share * p.pitch, tile);
   const int64_t base = (int64_t)a.B * a.G * p.tiles, blocks = ceil_div((int64_t)a.width * a.P, 32);
@@ -37,7 +41,7 @@ inline AttendPlan attend_plan(const sc_paged_attention& a, int cus) {
   return p;
 }
 
-inline int64_t attend_rows(const sc_paged_attention& a, const AttendPlan& p) { return (int64_t)a.B * a.G * p.tiles * 16 * p.nt; }
+inline int64_t attend_rows(const sc_paged_attention& a, const AttendPlan& p) { return (int64_t)a.B * a.G * p.tiles * p.rows(); }
 
 inline int64_t attend_workspace(const sc_paged_attention& a, int cus) {
   if (a.B == 0 || a.L == 0) return 0;

@@ -75,8 +75,199 @@ __device__ __forceinline__ uint32_t exponents_full(uint32_t w) {
   if constexpr (__is_same(T, __bf16)) return (w & 0x7f807f80u) + 0x00800080u;
   return (w & 0x7c007c00u) + 0x04000400u;
 }
+template <class T>
+__device__ __forceinline__ bool any_full(uint32_t w) {
+  return __any((w & (sizeof(T) == 4 ? 0x80000000u : 0x80008000u)) != 0);
+}
 
 typedef uint32_t W4 __attribute__((ext_vector_type(4)));
+
+// ---- What both kernels do with 16 NT rows and 32 keys
+//
+// A lane has row `col` of each of its NT tiles and, of a block of 32 keys, those that key_of says.
+template <class T, int DT, int NT>
+struct Rows {
+  typedef typename Frag<T>::type V;
+  static constexpr int N = Frag<T>::N, KF = DT / (4 * N), VF = kBlock / (4 * N), DM = DT / 16;
+  static constexpr bool kWide = sizeof(T) == 4;
+  // fp16's weights lie below 2^14: what is 2^-20 of the largest is still a normal number
+  static constexpr float kLift = __is_same(T, _Float16) ? 6.0f : 0.0f;
+
+  const sc_paged_attention& a;
+  const Reach r;
+  const int part, col;
+  int head[NT], pos[NT], low[NT], pre[NT], most_key[NT];  // the row's head, position, and the keys that it sees
+  float slope[NT];
+  V q[NT][KF];
+  F4 o[DM][NT];                        // dims 16 d + 4 part + 0..3, unnormalised
+  F4 total[NT];                        // sum of the weights (fp32: of the lane's own keys, in the first)
+  float top[NT], use[NT];              // the running maximum (in units of log 2), and what is subtracted from scores
+
+  static __device__ __forceinline__ int key_of(int lanes, int u, int i) { return kWide ? 16 * u + 4 * lanes + i : 8 * lanes + 4 * u + i; }
+  static __device__ __forceinline__ int key_row(int u, int m) { return kWide ? 16 * u + m : 8 * (m >> 2) + 4 * u + (m & 3); }  // of row m of tile u
+
+  __device__ __forceinline__ Rows(const sc_paged_attention& a_, const Reach& r_, int b, int g, int row0, int pitch, int lane)
+      : a(a_), r(r_), part(lane >> 4), col(lane & 15) {
+    const int share = a.H / a.G;
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+      const int row = row0 + t * 16 + col, h = row / pitch, i = row - h * pitch;
+      const bool live = h < share && i < r.len;
+      pos[t] = live ? r.past + i : -1;
+      low[t] = a.window ? pos[t] - a.window + 1 : 0;
+      pre[t] = live ? r.prefix : 0;
+      most_key[t] = min(pos[t], r.end - 1);
+      head[t] = min(g * share + h, a.H - 1);
+      slope[t] = a.slopes ? a.slopes[head[t]] * kLog2e : 0.0f;
+      const T* p = static_cast<const T*>(a.q) + b * a.q_batch + (int64_t)head[t] * a.D * a.q_channel + i;
+#pragma unroll
+      for (int f = 0; f < KF; f++)
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+          const int d = f * 4 * N + part * N + j;
+          q[t][f][j] = live && d < a.D ? p[d * a.q_channel] : T(0.0f);
+        }
+#pragma unroll
+      for (int d = 0; d < DM; d++) o[d][t] = F4{0.0f, 0.0f, 0.0f, 0.0f};
+      total[t] = F4{0.0f, 0.0f, 0.0f, 0.0f};
+      top[t] = -kInf, use[t] = -kLift;
+    }
+  }
+
+  // Whether every row sees all of keys k0 .. k0+31 (`miss`: halves of them that are on no page).
+  __device__ __forceinline__ bool whole(int k0, int miss) const {
+    const int first = r.past + r.first, last = r.past + r.last;
+    return !miss && k0 + kBlock <= r.end &&
+           (k0 + kBlock <= r.prefix || (k0 + kBlock - 1 <= first && (!a.window || k0 >= last - a.window + 1)));
+  }
+  __device__ __forceinline__ bool hidden(int lanes, int k0, int miss, int u, int t, int i) const {
+    const int key = k0 + key_of(lanes, u, i);
+    return (((miss >> (kWide ? u : lanes >> 1)) & 1) != 0) | ((key >= pre[t]) & ((key > most_key[t]) | (key < low[t])));
+  }
+
+  // From the products q . k to the weights, in s and (rounded) in p; sums and totals follow the maximum.
+  __device__ __forceinline__ void weigh(F4 (&s)[2][NT], V (&p)[NT][VF], int k0, int miss, bool all) {
+    float scale = a.scale * kLog2e;
+    if (a.cap > 0.0f || a.slopes || !(scale > 0.0f)) {  // else the maximum is looked for among the products themselves
+      const float by = a.cap > 0.0f ? a.scale / a.cap : scale, cap = a.cap * kLog2e;
+#pragma unroll
+      for (int u = 0; u < 2; u++)
+#pragma unroll
+        for (int t = 0; t < NT; t++) {
+          F4 v = s[u][t];
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            v[i] *= by;
+            if (a.cap > 0.0f) v[i] = cap * tanh_of<T>(v[i]);
+            if (a.slopes) v[i] -= slope[t] * fabsf((float)(pos[t] - k0 - key_of(part, u, i)));
+          }
+          s[u][t] = v;
+        }
+      scale = 1.0f;
+    }
+    // without branches: elements of a vector that were written under a lane's condition came out wrong here
+    if (!all)
+#pragma unroll
+      for (int u = 0; u < 2; u++)
+#pragma unroll
+        for (int t = 0; t < NT; t++) {
+          F4 v = s[u][t];
+#pragma unroll
+          for (int i = 0; i < 4; i++) v[i] = hidden(part, k0, miss, u, t, i) ? -kInf : v[i];
+          s[u][t] = v;
+        }
+    // the maximum moves where a score passes it by 2^8 (the first ones do)
+    bool moves = false;
+    float most[NT];
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+      most[t] = fmaxf(fmaxf(fmaxf(s[0][t][0], s[0][t][1]), fmaxf(s[0][t][2], s[0][t][3])),
+                      fmaxf(fmaxf(s[1][t][0], s[1][t][1]), fmaxf(s[1][t][2], s[1][t][3]))) * scale;
+      moves |= most[t] > top[t] + 8.0f;
+    }
+    if (__any(moves))
+#pragma unroll
+      for (int t = 0; t < NT; t++) {
+        const float m = fmaxf(top[t], column_max(most[t])), u = m == -kInf ? 0.0f : m;
+        const float factor = top[t] == -kInf ? 0.0f : exp2_fast(top[t] - u);
+        top[t] = m, use[t] = u - kLift;
+        total[t] *= factor;
+#pragma unroll
+        for (int d = 0; d < DM; d++) o[d][t] *= factor;
+      }
+#pragma unroll
+    for (int t = 0; t < NT; t++)
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        F4 w = s[u][t];
+#pragma unroll
+        for (int i = 0; i < 4; i++) w[i] = exp2_fast(fmaf(w[i], scale, -use[t]));
+        s[u][t] = w;
+        if (kWide) total[t][0] += (w[0] + w[1]) + (w[2] + w[3]);
+#pragma unroll
+        for (int i = 0; i < 4; i++) p[t][kWide ? u : 0][kWide ? i : 4 * u + i] = T(w[i]);
+      }
+    // the rounded weights are summed as they are used: a sum over rows of ones on the matrix cores
+    if constexpr (!kWide) {
+      V ones;
+#pragma unroll
+      for (int j = 0; j < N; j++) ones[j] = T(1.0f);
+#pragma unroll
+      for (int t = 0; t < NT; t++) total[t] = mma(ones, p[t][0], total[t]);
+    }
+  }
+
+  __device__ __forceinline__ float sum_of(int t) const { return kWide ? column_sum(total[t][0]) : total[t][0]; }
+
+  // o += the weights times the values, one key after another and only where a row sees it: 0 times infinity is
+  // no 0.  `w`: 16 x 33 floats of LDS for this wavefront; value(d, key).
+  template <class Value>
+  __device__ __forceinline__ void one_by_one(const F4 (&s)[2][NT], float* w, int k0, int miss, Value value) {
+    int lanes = part;
+    asm volatile("" : "+v"(lanes));  // keeps what is made of it out of the loop's registers
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+#pragma unroll
+      for (int u = 0; u < 2; u++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) w[col * 33 + key_of(lanes, u, i)] = hidden(lanes, k0, miss, u, t, i) ? -1.0f : s[u][t][i];
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+      for (int key = 0; key < kBlock; key++) {
+        const float weight = w[col * 33 + key];
+#pragma unroll
+        for (int d = 0; d < DM; d++) {
+          F4 v = o[d][t];
+#pragma unroll
+          for (int i = 0; i < 4; i++) v[i] = weight >= 0.0f ? fmaf(weight, value(d * 16 + 4 * lanes + i, key), v[i]) : v[i];
+          o[d][t] = v;
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+};
+
+// The blocks of `size` keys that a tile's rows see: those of the prefix, then those that the window leaves.
+struct Blocks {
+  int prefix, jump, count;
+  __device__ __forceinline__ Blocks(const sc_paged_attention& a, const Reach& r, int size) {
+    const int until = r.any ? max(min(r.past + r.last + 1, r.end), r.prefix) : 0;
+    const int from = r.any && a.window ? min(max(r.past + r.first - a.window + 1, 0), until) / size : 0;
+    prefix = (r.prefix + size - 1) / size;
+    jump = max(from - prefix, 0);
+    count = r.any ? max((until + size - 1) / size - jump, 0) : 0;
+  }
+  __device__ __forceinline__ int at(int n) const { return n < prefix ? n : n + jump; }
+};
+
+// Page `at` of a sequence's table, negative where there is none.
+__device__ __forceinline__ int page_of(const sc_paged_attention& a, const int32_t* table, int at) {
+  const int p = at < a.width ? table[at] : -1;
+  return p < a.pages ? p : -1;
+}
 
 // ---- Few rows: every wavefront has its own blocks of keys
 //
@@ -85,14 +276,12 @@ typedef uint32_t W4 __attribute__((ext_vector_type(4)));
 // way while one is computed, and their sums are joined at the end.
 template <class T, int DT, int NT>
 __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2) void attend_direct(const sc_paged_attention a, const Cut cut) {
-  typedef typename Frag<T>::type V;
-  constexpr int N = Frag<T>::N, KF = DT / (4 * N), VF = kBlock / (4 * N), DM = DT / 16;
-  constexpr bool kWide = sizeof(T) == 4;
-  // fp16's weights lie below 2^14: what is 2^-20 of the largest is still a normal number
-  constexpr float kLift = __is_same(T, _Float16) ? 6.0f : 0.0f;
+  typedef Rows<T, DT, NT> R;
+  typedef typename R::V V;
+  constexpr int N = R::N, KF = R::KF, VF = R::VF, DM = R::DM;
   constexpr int kPitch = DT + 4;
   constexpr bool kAhead = DT * sizeof(T) < 1024;  // else a block's keys and values alone fill the registers
-  __shared__ float lds[4 * 16 * kPitch > 4 * 16 * NT * 33 ? 4 * 16 * kPitch : 4 * 16 * NT * 33];
+  __shared__ float lds[4 * 16 * (kPitch > 33 ? kPitch : 33)];
   __shared__ float2 tops[4][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, part = lane >> 4;
   int id = xcd_logical(blockIdx.x, gridDim.x);
@@ -102,39 +291,8 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
   id /= cut.tiles;
   const int g = id % a.G, b = id / a.G, share = a.H / a.G, row0 = tile * 16 * NT;
   const Reach r = reach_of(a, b, row0, 16 * NT, cut.pitch);
-
-  // the rows' positions and queries
-  int pos[NT], head[NT], low[NT], pre[NT], most_key[NT];
-  bool live[NT], there[NT];
-  V q[NT][KF];
-#pragma unroll
-  for (int t = 0; t < NT; t++) {
-    const int row = row0 + t * 16 + col, h = row / cut.pitch, i = row - h * cut.pitch;
-    there[t] = h < share && i < a.L;
-    live[t] = there[t] && i < r.len;
-    pos[t] = live[t] ? r.past + i : -1;
-    low[t] = a.window ? pos[t] - a.window + 1 : 0;
-    pre[t] = live[t] ? r.prefix : 0;
-    most_key[t] = min(pos[t], r.end - 1);
-    head[t] = min(g * share + h, a.H - 1);
-    const T* p = static_cast<const T*>(a.q) + b * a.q_batch + (int64_t)head[t] * a.D * a.q_channel + i;
-#pragma unroll
-    for (int f = 0; f < KF; f++)
-#pragma unroll
-      for (int j = 0; j < N; j++) {
-        const int d = f * 4 * N + part * N + j;
-        q[t][f][j] = live[t] && d < a.D ? p[d * a.q_channel] : T(0.0f);
-      }
-  }
-
-  // the blocks: those of the prefix, then those that the window leaves
-  const int last_pos = r.past + r.last, first_pos = r.past + r.first;
-  const int until = r.any ? max(min(last_pos + 1, r.end), r.prefix) : 0;
-  const int from = r.any && a.window ? min(max(first_pos - a.window + 1, 0), until) / kBlock : 0;
-  const int np = (r.prefix + kBlock - 1) / kBlock, jump = max(from - np, 0);
-  const int blocks = r.any ? max((until + kBlock - 1) / kBlock - jump, 0) : 0;
-  const int per = (blocks + cut.splits - 1) / cut.splits, stop = min(blocks, (split + 1) * per);
-  auto block_at = [&](int n) { return n < np ? n : n + jump; };
+  const Blocks blocks(a, r, kBlock);
+  const int per = (blocks.count + cut.splits - 1) / cut.splits, stop = min(blocks.count, (split + 1) * per);
   const int shift = 31 - __builtin_clz(a.P);
 
   // the pages of a block's two halves, negative where there is none (page 0 is read then, and hidden)
@@ -142,23 +300,20 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
     int first, second, key;
   };
   const int32_t* table = a.table + b * a.table_batch;
-  auto page = [&](int at) {
-    const int p = at < a.width ? table[at] : -1;
-    return p < a.pages ? p : -1;
+  auto find = [&](int blk) {
+    return Where{page_of(a, table, blk * kBlock >> shift), page_of(a, table, (blk * kBlock + 16) >> shift), blk * kBlock};
   };
-  auto find = [&](int blk) { return Where{page(blk * kBlock >> shift), page((blk * kBlock + 16) >> shift), blk * kBlock}; };
   // of key `key` of the block: its dims, and its values of dim 0
   const T* k_head = static_cast<const T*>(a.k_pages) + (int64_t)g * a.P * a.D;
   const T* v_head = static_cast<const T*>(a.v_pages) + (int64_t)g * a.P * a.D;
-  auto page_of = [&](Where w, int key) { return max(key & 16 ? w.second : w.first, 0); };
-  auto key_at = [&](Where w, int key) { return k_head + page_of(w, key) * a.k_page + ((w.key + key) & (a.P - 1)) * a.D; };
-  auto value_at = [&](Where w, int key) { return v_head + page_of(w, key) * a.v_page + ((w.key + key) & (a.P - 1)); };
+  auto page_at = [&](Where w, int key) { return max(key & 16 ? w.second : w.first, 0); };
+  auto key_at = [&](Where w, int key) { return k_head + page_at(w, key) * a.k_page + ((w.key + key) & (a.P - 1)) * a.D; };
+  auto value_at = [&](Where w, int key) { return v_head + page_at(w, key) * a.v_page + ((w.key + key) & (a.P - 1)); };
   V kf[2][KF], vf[DM][VF];
   auto load_k = [&](Where w) {
 #pragma unroll
     for (int t = 0; t < 2; t++) {
-      const int key = kWide ? 16 * t + col : 8 * (col >> 2) + 4 * t + (col & 3);
-      const T* p = key_at(w, key);
+      const T* p = key_at(w, R::key_row(t, col));
 #pragma unroll
       for (int f = 0; f < KF; f++) kf[t][f] = *reinterpret_cast<const V*>(p + min(f * 4 * N + part * N, a.D - N));
     }
@@ -172,37 +327,26 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
   auto load_v = [&](Where w) {
 #pragma unroll
     for (int f = 0; f < VF; f++) {
-      const int key = f * 4 * N + part * N;
-      const T* p = value_at(w, key);
+      const T* p = value_at(w, f * 4 * N + part * N);
 #pragma unroll
       for (int d = 0; d < DM; d++) vf[d][f] = *reinterpret_cast<const V*>(p + min(d * 16 + col, a.D - 1) * a.P);
     }
   };
 
-  F4 o[DM][NT];
-  float top[NT], use[NT], sum[NT], slope[NT];
-#pragma unroll
-  for (int t = 0; t < NT; t++) {
-#pragma unroll
-    for (int d = 0; d < DM; d++) o[d][t] = F4{0.0f, 0.0f, 0.0f, 0.0f};
-    top[t] = -kInf, use[t] = -kLift, sum[t] = 0.0f;
-    slope[t] = a.slopes ? a.slopes[head[t]] * kLog2e : 0.0f;
-  }
-  const float scale = a.cap > 0.0f ? a.scale / a.cap : a.scale * kLog2e, cap = a.cap * kLog2e;
-
   int n = split * per + wave;
   Where at, next;
   if (n < stop) {
-    at = find(block_at(n));
+    at = find(blocks.at(n));
     if (kAhead) {
       load_k(at);
       load_v(at);
     }
   }
+  R rows(a, r, b, g, row0, cut.pitch, lane);
   for (; n < stop; n += 4) {
     const int k0 = at.key, miss = (at.first < 0 ? 1 : 0) | (at.second < 0 ? 2 : 0);
     const bool more = n + 4 < stop;
-    if (more) next = find(block_at(n + 4));
+    if (more) next = find(blocks.at(n + 4));
     if (!kAhead) load_k(at);
     F4 s[2][NT];
 #pragma unroll
@@ -211,85 +355,23 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
       for (int t = 0; t < NT; t++) {
         s[u][t] = F4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int f = 0; f < KF; f++) s[u][t] = mma(kf[u][f], q[t][f], s[u][t]);
+        for (int f = 0; f < KF; f++) s[u][t] = mma(kf[u][f], rows.q[t][f], s[u][t]);
       }
     if (kAhead && more) load_k(next);
     if (!kAhead) load_v(at);
-    // scores in units of log 2
-    auto key_of = [&](int lanes, int u, int i) { return k0 + (kWide ? 16 * u + 4 * lanes + i : 8 * lanes + 4 * u + i); };
-#pragma unroll
-    for (int u = 0; u < 2; u++)
-#pragma unroll
-      for (int t = 0; t < NT; t++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          float v = s[u][t][i] * scale;
-          if (a.cap > 0.0f) v = cap * tanh_of<T>(v);
-          if (a.slopes) v -= slope[t] * fabsf((float)(pos[t] - key_of(part, u, i)));
-          s[u][t][i] = v;
-        }
-    const bool whole = !miss && k0 + kBlock <= r.end &&
-                       (k0 + kBlock <= r.prefix || (k0 + kBlock - 1 <= first_pos && (!a.window || k0 >= last_pos - a.window + 1)));
-    // all of it without branches: elements of a vector that were written under a lane's condition came out wrong here
-    auto hidden = [&](int lanes, int u, int t, int i) {
-      const int key = key_of(lanes, u, i);
-      return (((miss >> (kWide ? u : lanes >> 1)) & 1) != 0) | ((key >= pre[t]) & ((key > most_key[t]) | (key < low[t])));
-    };
-    if (!whole)
-#pragma unroll
-      for (int u = 0; u < 2; u++)
-#pragma unroll
-        for (int t = 0; t < NT; t++) {
-          F4 v = s[u][t];
-#pragma unroll
-          for (int i = 0; i < 4; i++) v[i] = hidden(part, u, t, i) ? -kInf : v[i];
-          s[u][t] = v;
-        }
-    // the maximum moves where a score passes it by 2^8 (the first ones do)
-    bool moves = false;
-    float most[NT];
-#pragma unroll
-    for (int t = 0; t < NT; t++) {
-      most[t] = -kInf;
-#pragma unroll
-      for (int i = 0; i < 4; i++) most[t] = fmaxf(most[t], fmaxf(s[0][t][i], s[1][t][i]));
-      moves |= most[t] > top[t] + 8.0f;
-    }
-    if (__any(moves))
-#pragma unroll
-      for (int t = 0; t < NT; t++) {
-        const float m = fmaxf(top[t], column_max(most[t])), u = m == -kInf ? 0.0f : m;
-        const float factor = top[t] == -kInf ? 0.0f : exp2_fast(top[t] - u);
-        top[t] = m, use[t] = u - kLift;
-        sum[t] *= factor;
-#pragma unroll
-        for (int d = 0; d < DM; d++)
-#pragma unroll
-          for (int i = 0; i < 4; i++) o[d][t][i] *= factor;
-      }
+    const bool whole = rows.whole(k0, miss);
     V p[NT][VF];
-#pragma unroll
-    for (int t = 0; t < NT; t++)
-#pragma unroll
-      for (int u = 0; u < 2; u++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const float w = exp2_fast(s[u][t][i] - use[t]);
-          sum[t] += w;
-          s[u][t][i] = w;
-          p[t][kWide ? u : 0][kWide ? i : 4 * u + i] = T(w);
-        }
+    rows.weigh(s, p, k0, miss, whole);
     bool odd = false;
     if (!whole) {
-      // nothing that is not there reaches the product, and what only some rows see is looked at: 0 times
-      // infinity is no 0
+      // nothing that is not there reaches the product, and what only some rows see is looked at
       uint32_t full = 0;
 #pragma unroll
       for (int f = 0; f < VF; f++) {
         const int key = f * 4 * N + part * N, left = miss >> (key >> 4 & 1) & 1 ? 0 : r.end - k0 - key;
         W4 keep;
 #pragma unroll
-        for (int j = 0; j < 4; j++) keep[j] = kWide ? (j < left ? ~0u : 0u) : (2 * j + 1 < left ? ~0u : 2 * j < left ? 0xffffu : 0u);
+        for (int j = 0; j < 4; j++) keep[j] = R::kWide ? (j < left ? ~0u : 0u) : (2 * j + 1 < left ? ~0u : 2 * j < left ? 0xffffu : 0u);
 #pragma unroll
         for (int d = 0; d < DM; d++) {
           const W4 v = __builtin_bit_cast(W4, vf[d][f]) & keep;
@@ -298,46 +380,19 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
           for (int j = 0; j < 4; j++) full |= exponents_full<T>(v[j]);
         }
       }
-      odd = __any((full & (kWide ? 0x80000000u : 0x80008000u)) != 0);
+      odd = any_full<T>(full);
     }
     if (__builtin_expect(odd, false)) {
-      int lanes = part;
-      asm volatile("" : "+v"(lanes));  // keeps what is made of it below out of the loop's registers
-      float* w = lds + wave * (16 * NT * 33);
-#pragma unroll
-      for (int t = 0; t < NT; t++)
-#pragma unroll
-        for (int u = 0; u < 2; u++)
-#pragma unroll
-          for (int i = 0; i < 4; i++) w[(t * 16 + col) * 33 + key_of(lanes, u, i) - k0] = hidden(lanes, u, t, i) ? -1.0f : s[u][t][i];
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-      for (int key = 0; key < kBlock; key++) {
-        const T* pv = value_at(at, key);
-        if (k0 + key >= r.end || (miss >> (key >> 4) & 1)) continue;
-        float weight[NT];
-#pragma unroll
-        for (int t = 0; t < NT; t++) weight[t] = w[(t * 16 + col) * 33 + key];
-#pragma unroll
-        for (int d = 0; d < DM; d++)
-#pragma unroll
-          for (int i = 0; i < 4; i++) {
-            const float val = (float)pv[min(d * 16 + 4 * lanes + i, a.D - 1) * a.P];
-#pragma unroll
-            for (int t = 0; t < NT; t++)
-              o[d][t][i] = weight[t] >= 0.0f ? fmaf(weight[t], val, o[d][t][i]) : o[d][t][i];
-          }
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+      rows.one_by_one(s, lds + wave * (16 * 33), k0, miss, [&](int d, int key) {
+        return k0 + key < r.end ? (float)value_at(at, key)[min(d, a.D - 1) * a.P] : 0.0f;
+      });
     } else {
 #pragma unroll
       for (int f = 0; f < VF; f++)
 #pragma unroll
         for (int d = 0; d < DM; d++)
 #pragma unroll
-          for (int t = 0; t < NT; t++) o[d][t] = mma(vf[d][f], p[t][f], o[d][t]);
+          for (int t = 0; t < NT; t++) rows.o[d][t] = mma(vf[d][f], p[t][f], rows.o[d][t]);
     }
     if (kAhead && more) load_v(next);
     at = next;
@@ -349,9 +404,9 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
   for (int t = 0; t < NT; t++) {
     __syncthreads();
 #pragma unroll
-    for (int d = 0; d < DM; d++) *reinterpret_cast<F4*>(&lds[(wave * 16 + col) * kPitch + d * 16 + part * 4]) = o[d][t];
-    const float total = column_sum(sum[t]);
-    if (part == 0) tops[wave][col] = make_float2(top[t], total);
+    for (int d = 0; d < DM; d++) *reinterpret_cast<F4*>(&lds[(wave * 16 + col) * kPitch + d * 16 + part * 4]) = rows.o[d][t];
+    const float total = rows.sum_of(t);
+    if (part == 0) tops[wave][col] = make_float2(rows.top[t], total);
     __syncthreads();
     const int at_row = row0 + t * 16 + row, h = at_row / cut.pitch, i = at_row - h * cut.pitch;
     if (h >= share || i >= a.L) continue;
@@ -370,7 +425,8 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
     none = none | (i >= r.len);  // (where whole blocks are seen, rows that are not there saw them too)
     const int64_t ws_row = ((int64_t)(b * a.G + g) * cut.tiles + tile) * (16 * NT) + t * 16 + row;
     const float by = cut.splits > 1 ? 1.0f : none ? 0.0f : seen ? 1.0f / l : __builtin_nanf("");
-    if (cut.splits > 1 && piece == 0) cut.tops[ws_row * cut.splits + split] = make_float2(none ? -kInf : m, none ? 0.0f : seen ? l : __builtin_nanf(""));
+    if (cut.splits > 1 && piece == 0)
+      cut.tops[ws_row * cut.splits + split] = make_float2(none ? -kInf : m, none ? 0.0f : seen ? l : __builtin_nanf(""));
     const int64_t out = b * a.out_batch + (int64_t)(g * share + h) * a.D * a.out_channel + i;
     for (int d = piece * (DT / 16); d < min((piece + 1) * (DT / 16), a.D); d++) {
       float v = 0.0f;
@@ -383,6 +439,222 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
         static_cast<float*>(a.out)[out + d * a.out_channel] = v;
       else
         static_cast<T*>(a.out)[out + d * a.out_channel] = T(v);
+    }
+  }
+}
+
+// ---- Many rows: the wavefronts share the keys
+//
+// A workgroup has 64 NT rows of one head of keys, 16 NT a wavefront, and walks its piece of the context in tiles of KT
+// keys, which it copies from the pages to LDS without passing registers, one tile ahead.  In LDS a row's
+// 16-byte pieces are dealt out by an exclusive or with the row, so that the sixteen rows that a read takes
+// lie in sixteen different places of 256 bytes.
+
+// 16 bytes a lane from its address to LDS byte address `to` + 16 * lane (to: the same in all lanes).  Written
+// as asm so that the compiler does not wait for it before every LDS read; the wait is at the tile's end.
+__device__ __forceinline__ void to_lds(uint32_t to, const void* from) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, off"
+      :
+      : "s"(to), "v"(from)
+      : "memory", "m0");
+}
+
+template <class T, int DT>
+struct Stage {
+  static constexpr int KT = DT * sizeof(T) <= 256 ? 64 : 32;       // keys
+  static constexpr int kKeyRow = DT * sizeof(T), kValueRow = KT * sizeof(T);  // bytes of a row: a key's dims, a dim's values
+  static constexpr int kKeys = KT * kKeyRow, kBytes = 2 * kKeys;   // of a tile: its keys, then its values
+  static constexpr int CK = kKeyRow / 16, CV = kValueRow / 16;     // pieces of a row
+  // where piece c of a row lies
+  static __device__ __forceinline__ int key_piece(int key, int c) {
+    const int m = sizeof(T) == 4 ? key & 15 : (key >> 3 & 3) << 2 | (key & 3);  // the row of a product's tile
+    return c ^ (CK >= 16 ? m : m >> 1);
+  }
+  static __device__ __forceinline__ int value_piece(int d, int c) { return c ^ (CV >= 16 ? d & 15 : CV == 8 ? d >> 1 & 7 : d >> 2 & 3); }
+};
+
+template <class T, int DT, int NT>
+__global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2) void attend_staged(const sc_paged_attention a, const Cut cut) {
+  typedef Rows<T, DT, NT> R;
+  typedef Stage<T, DT> S;
+  typedef typename R::V V;
+  constexpr int N = R::N, KF = R::KF, VF = R::VF, DM = R::DM, KT = S::KT;
+  constexpr int KI = S::kKeys / 4096;                      // copies of a wavefront's for the keys, and as many for the values
+  constexpr int RK = 64 / S::CK, RV = 64 / S::CV;          // rows of one copy
+  __shared__ __align__(256) char lds[2 * S::kBytes + 4 * 16 * 33 * 4];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, part = lane >> 4;
+  // the rows that see most come first, and a head of keys stays on its XCDs
+  const int heads = a.B * a.G, share = a.H / a.G;
+  int id = blockIdx.x;
+  const int bg = id % heads;
+  id /= heads;
+  const int split = id % cut.splits;
+  id /= cut.splits;
+  const int each = cut.pitch / (64 * NT);  // tiles of a head, or 0 where a tile has several
+  const int tile = each ? id % share * each + (each - 1 - id / share) : id;
+  const int g = bg % a.G, b = bg / a.G;
+  const Reach reach = reach_of(a, b, tile * 64 * NT, 64 * NT, cut.pitch);
+  const int row0 = tile * 64 * NT + wave * 16 * NT;
+  const Reach r = reach_of(a, b, row0, 16 * NT, cut.pitch);
+  const Blocks tiles(a, reach, KT);
+  const int per = (tiles.count + cut.splits - 1) / cut.splits, stop = min(tiles.count, (split + 1) * per);
+  const int shift = 31 - __builtin_clz(a.P);
+  const int32_t* table = a.table + b * a.table_batch;
+  const uint32_t base = (uint32_t)(size_t)lds;
+
+  // this wavefront's copies: rows of keys RK (4 i + wave) .., rows of values RV (4 i + wave) ..
+  const int kc = lane % S::CK, kr = lane / S::CK, vr = lane / S::CV;
+  const int vc = S::value_piece(RV * wave + vr, lane % S::CV) * N;  // the same for every i
+  const T* k_head = static_cast<const T*>(a.k_pages) + (int64_t)g * a.P * a.D;
+  const T* v_head = static_cast<const T*>(a.v_pages) + (int64_t)g * a.P * a.D;
+  // which sixteens of the tile's keys are on no page
+  auto copy = [&](int k0, int buffer) {
+    int page[KT / 16], miss = 0;
+#pragma unroll
+    for (int h = 0; h < KT / 16; h++) {
+      page[h] = page_of(a, table, (k0 + 16 * h) >> shift);
+      if (page[h] < 0) page[h] = 0, miss |= 1 << h;
+    }
+    const uint32_t to = base + buffer * S::kBytes + wave * 1024;
+#pragma unroll
+    for (int i = 0; i < KI; i++) {
+      const int first = RK * (4 * i + wave), key = first + kr, c = S::key_piece(key, kc) * N;
+      int pg = page[0];
+#pragma unroll
+      for (int h = 1; h < KT / 16; h++) pg = first >> 4 == h ? page[h] : pg;
+      const T* from = k_head + pg * a.k_page + ((k0 + key) & (a.P - 1)) * a.D + c;
+      if (DT == 64 || a.D == DT || c < a.D) {
+        if (c < a.D) to_lds(to + i * 4096, from);
+      }
+    }
+    int pg = page[0];
+#pragma unroll
+    for (int h = 1; h < KT / 16; h++) pg = vc >> 4 == h ? page[h] : pg;
+    const T* from = v_head + pg * a.v_page + ((k0 + vc) & (a.P - 1));
+#pragma unroll
+    for (int i = 0; i < KI; i++) {
+      const int d = RV * (4 * i + wave) + vr;
+      if (d < a.D) to_lds(to + S::kKeys + i * 4096, from + d * a.P);
+    }
+    return miss;
+  };
+  int n = split * per, miss = 0, k0 = tiles.at(n) * KT;
+  if (a.D != DT) {  // dims past D are never copied: both products take them as 0
+    for (int e = threadIdx.x; e < 2 * S::kBytes / 16; e += 256) reinterpret_cast<W4*>(lds)[e] = W4{0, 0, 0, 0};
+    __syncthreads();
+  }
+  if (n < stop) miss = copy(k0, 0);
+  R rows(a, r, b, g, row0, cut.pitch, lane);
+  // the rows' own part of the tile's keys
+  const int until = r.any ? max(min(r.past + r.last + 1, r.end), r.prefix) : 0;
+  const int from = r.any && a.window ? r.past + r.first - a.window + 1 : 0;
+  int buffer = 0;
+  for (; n < stop; n++, buffer ^= 1) {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");  // this tile is there, and nobody reads the one before
+    const int here = k0, gone = miss;
+    if (n + 1 < stop) {
+      k0 = tiles.at(n + 1) * KT;
+      miss = copy(k0, buffer ^ 1);
+    }
+    char* keys = lds + buffer * S::kBytes;
+    char* values = keys + S::kKeys;
+    if (here + KT > r.end || gone) {  // nothing that is not there reaches the product
+      for (int e = threadIdx.x; e < S::kKeys / 16; e += 256) {
+        const int d = e / S::CV, key = S::value_piece(d, e % S::CV) * N, left = gone >> (key >> 4) & 1 ? 0 : r.end - here - key;
+        if (left >= N) continue;
+        W4 v = reinterpret_cast<W4*>(values)[e];
+#pragma unroll
+        for (int j = 0; j < 4; j++) v[j] &= R::kWide ? (j < left ? ~0u : 0u) : (2 * j + 1 < left ? ~0u : 2 * j < left ? 0xffffu : 0u);
+        reinterpret_cast<W4*>(values)[e] = v;
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    }
+#pragma unroll
+    for (int kb = 0; kb < KT / kBlock; kb++) {
+      const int at = here + kb * kBlock, lost = gone >> (2 * kb) & 3;
+      if (at >= until || (at + kBlock <= from && at >= r.prefix)) continue;
+      F4 s[2][NT];
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        const int key = kb * kBlock + R::key_row(u, col);
+        V kf[KF];
+#pragma unroll
+        for (int f = 0; f < KF; f++) kf[f] = *reinterpret_cast<const V*>(keys + key * S::kKeyRow + S::key_piece(key, 4 * f + part) * 16);
+#pragma unroll
+        for (int t = 0; t < NT; t++) {
+          s[u][t] = F4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int f = 0; f < KF; f++) s[u][t] = mma(kf[f], rows.q[t][f], s[u][t]);
+        }
+      }
+      const bool whole = rows.whole(at, lost);
+      V p[NT][VF];
+      rows.weigh(s, p, at, lost, whole);
+      auto value = [&](int d, int f) {
+        return *reinterpret_cast<const V*>(values + d * S::kValueRow + S::value_piece(d, (kb * VF + f) * 4 + part) * 16);
+      };
+      bool odd = false;
+      if (!whole) {
+        uint32_t full = 0;
+#pragma unroll
+        for (int f = 0; f < VF; f++)
+#pragma unroll
+          for (int d = 0; d < DM; d++) {
+            const W4 v = __builtin_bit_cast(W4, value(d * 16 + col, f));
+#pragma unroll
+            for (int j = 0; j < 4; j++) full |= exponents_full<T>(v[j]);
+          }
+        odd = any_full<T>(full);
+      }
+      if (__builtin_expect(odd, false)) {
+        float* w = reinterpret_cast<float*>(lds + 2 * S::kBytes) + wave * (16 * 33);
+        rows.one_by_one(s, w, at, lost, [&](int d, int key) {
+          const int k = kb * kBlock + key;
+          return (float)*reinterpret_cast<const T*>(values + d * S::kValueRow + S::value_piece(d, k / N) * 16 + k % N * sizeof(T));
+        });
+      } else {
+#pragma unroll
+        for (int f = 0; f < VF; f++)
+#pragma unroll
+          for (int d = 0; d < DM; d++) {
+            const V v = value(d * 16 + col, f);
+#pragma unroll
+            for (int t = 0; t < NT; t++) rows.o[d][t] = mma(v, p[t][f], rows.o[d][t]);
+          }
+      }
+    }
+  }
+
+#pragma unroll
+  for (int t = 0; t < NT; t++) {
+    const int row = row0 + t * 16 + col, h = row / cut.pitch, i = row - h * cut.pitch;
+    const float total = rows.sum_of(t);
+    if (h >= share || i >= a.L) continue;
+    const bool none = (total == 0.0f) | (i >= r.len);
+    if (cut.splits > 1) {
+      const int64_t at = ((int64_t)bg * cut.tiles * (64 * NT) + row) * cut.splits + split;
+      if (part == 0) cut.tops[at] = make_float2(none ? -kInf : rows.top[t], none ? 0.0f : total);
+#pragma unroll
+      for (int d = 0; d < DM; d++)
+        if (d * 16 + part * 4 < a.D) *reinterpret_cast<F4*>(cut.sums + at * a.D + d * 16 + part * 4) = rows.o[d][t];
+    } else {
+      const float by = none ? 0.0f : 1.0f / total;
+      const int64_t out = b * a.out_batch + (int64_t)(g * share + h) * a.D * a.out_channel + i;
+#pragma unroll
+      for (int d = 0; d < DM; d++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          const int dim = d * 16 + part * 4 + j;
+          if (dim >= a.D) continue;
+          const float v = none ? 0.0f : rows.o[d][t][j] * by;
+          if (a.flags & SC_ATT_OUT_F32)
+            static_cast<float*>(a.out)[out + dim * a.out_channel] = v;
+          else
+            static_cast<T*>(a.out)[out + dim * a.out_channel] = T(v);
+        }
     }
   }
 }
@@ -431,8 +703,16 @@ int launch_direct(const sc_paged_attention& a, const AttendPlan& p, const Cut& c
   return (int)hipGetLastError();
 }
 
+template <class T, int DT, int NT>
+int launch_staged(const sc_paged_attention& a, const AttendPlan& p, const Cut& cut, hipStream_t st) {
+  const int64_t blocks = (int64_t)a.B * a.G * p.groups();
+  hipLaunchKernelGGL((attend_staged<T, DT, NT>), dim3((unsigned)blocks), dim3(256), 0, st, a, cut);
+  return (int)hipGetLastError();
+}
+
 template <class T, int DT>
 int launch_dims(const sc_paged_attention& a, const AttendPlan& p, const Cut& cut, hipStream_t st) {
+  if (p.staged) return launch_staged<T, DT, attend_staged_tiles(sizeof(T), DT)>(a, p, cut, st);
   constexpr int kMost = attend_most_tiles(sizeof(T), DT);
   if constexpr (kMost >= 4)
     if (p.nt == 4) return launch_direct<T, DT, 4>(a, p, cut, st);
@@ -452,7 +732,7 @@ int launch_type(const sc_paged_attention& a, int cus, hipStream_t st) {
   }
   const int e = a.D <= 64 ? launch_dims<T, 64>(a, p, cut, st) : a.D <= 128 ? launch_dims<T, 128>(a, p, cut, st) : launch_dims<T, 256>(a, p, cut, st);
   if (e || p.splits == 1) return e;
-  hipLaunchKernelGGL(attend_join<T>, dim3((unsigned)ceil_div(rows, 4)), dim3(256), 0, st, a, cut, 16 * p.nt);
+  hipLaunchKernelGGL(attend_join<T>, dim3((unsigned)ceil_div(rows, 4)), dim3(256), 0, st, a, cut, p.rows());
   return (int)hipGetLastError();
 }
 

@@ -35,8 +35,9 @@ def paged_attention(q, k_pages, v_pages, table, past, lengths=None, scale=None, 
     The error of a score: D + 3 roundings of the product's magnitudes; with a cap its tanh, off by 2^-22 (fp32: 4 U) of 1
     and of slope at most 1; of the bias 3 U of it; the product with log2(e), the difference from the
     maximum and exp2's own add 4 U of the largest magnitude of a score.  A weight is off by that and 4 U of itself,
-    and in the second product by a rounding to q's type, relative, or 2^-31 of the row's largest (fp16, whose
-    weights are 2^6 at the maximum and below: 2^-25 of them).  Maxima that trail by less than 2^8 only enlarge them."""
+    and (16-bit types) by a rounding to q's type, relative, or 2^-31 of the row's largest (fp16, whose
+    weights are 2^6 at the maximum and below: 2^-25 of them).  Maxima that trail by less than 2^8 only enlarge them.  A
+    relative error e_t of each weight moves sum p v / sum p by at most sum p |e_t| (|v| + |out|) / sum p."""
     dtype = q.dtype
     out_dtype = out_dtype or dtype
     Q, K, V = wide(q), wide(k_pages), wide(v_pages)
@@ -93,10 +94,10 @@ def paged_attention(q, k_pages, v_pages, table, past, lengths=None, scale=None, 
             o = (p @ vf) / torch.where(some, total, 1.0)
             rel = torch.where(seen, es, 0.0) + 4 * U * (largest + 1)
             num = ((p * (rel + weight_round + (T + 8) * U)) @ vf.abs()) / torch.where(some, total, 1.0)
-            den = (p * (rel + (T + 8) * U)).sum(1, keepdim=True) / torch.where(some, total, 1.0)
+            den = (p * (rel + weight_round + (T + 8) * U)).sum(1, keepdim=True) / torch.where(some, total, 1.0)
             e = num + den * o.abs() + 4 * U * o.abs()
             if dtype == torch.float16:
-                e = e + 2.0 ** -31 * ((seen.double() @ vf.abs()) / torch.where(some, total, 1.0))
+                e = e + 2.0 ** -31 * ((seen.double() @ vf.abs()) + seen.sum(1, keepdim=True) * o.abs()) / torch.where(some, total, 1.0)
             e = 1.05 * e  # second order: every relative error above is far below 0.05
             bad = (seen.double() @ (~ok).double()) > 0
             o = torch.where(some, o, 0.0).masked_fill(bad, math.nan)
