@@ -10,6 +10,8 @@
 // lane's eight results are eight (fp32: two times four) consecutive keys.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "attention.h"
 #include "attention_plan.h"
 #include "matrix_device.h"
@@ -68,17 +70,19 @@ __device__ __forceinline__ float tanh_of(float x) {
   return 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + exp2_fast(2.0f * kLog2e * x));
 }
 
-// A word of one or two values: the sign bits of the result say which exponents are full (infinities and NaN).
+// Words of one or two values.
 template <class T>
-__device__ __forceinline__ uint32_t exponents_full(uint32_t w) {
-  if constexpr (sizeof(T) == 4) return (w & 0x7f800000u) + 0x00800000u;
-  if constexpr (__is_same(T, __bf16)) return (w & 0x7f807f80u) + 0x00800080u;
-  return (w & 0x7c007c00u) + 0x04000400u;
-}
-template <class T>
-__device__ __forceinline__ bool any_full(uint32_t w) {
-  return __any((w & (sizeof(T) == 4 ? 0x80000000u : 0x80008000u)) != 0);
-}
+struct Bits {  // of each value: its sign, its exponent's highest and lowest, the number 1
+  static constexpr bool kWide = sizeof(T) == 4, kB = __is_same(T, __bf16);
+  static constexpr uint32_t kSigns = kWide ? 0x80000000u : 0x80008000u;
+  static constexpr uint32_t kExponents = kWide ? 0x7f800000u : kB ? 0x7f807f80u : 0x7c007c00u;
+  static constexpr uint32_t kOnes = kWide ? 0x3f800000u : kB ? 0x3f803f80u : 0x3c003c00u;
+  // the signs of these say which exponents are full (infinities and NaN), and which values are NaN
+  static __device__ __forceinline__ uint32_t full(uint32_t w) { return (w & kExponents) + (kExponents & ~(kExponents << 1)); }
+  static __device__ __forceinline__ uint32_t above_infinity(uint32_t w) { return (w & ~kSigns) + (~kSigns - kExponents); }
+  // all bits of the values whose sign is set
+  static __device__ __forceinline__ uint32_t spread(uint32_t w) { return kWide ? (uint32_t)((int32_t)w >> 31) : ((w >> 15) & 0x00010001u) * 0xffffu; }
+};
 
 typedef uint32_t W4 __attribute__((ext_vector_type(4)));
 
@@ -119,19 +123,44 @@ struct Rows {
       most_key[t] = min(pos[t], r.end - 1);
       head[t] = min(g * share + h, a.H - 1);
       slope[t] = a.slopes ? a.slopes[head[t]] * kLog2e : 0.0f;
-      const T* p = static_cast<const T*>(a.q) + b * a.q_batch + (int64_t)head[t] * a.D * a.q_channel + i;
+      // rows that are not there read ones that are: their results are dropped
+      const T* p = static_cast<const T*>(a.q) + b * a.q_batch + (int64_t)head[t] * a.D * a.q_channel + min(i, a.L - 1);
 #pragma unroll
-      for (int f = 0; f < KF; f++)
+      for (int f = 0; f < KF; f++) {
+        const int d0 = f * 4 * N + part * N;  // D is a multiple of N: all N dims are there or none
+        const T* from = p + min(d0, a.D - N) * a.q_channel;
+        V v;
 #pragma unroll
-        for (int j = 0; j < N; j++) {
-          const int d = f * 4 * N + part * N + j;
-          q[t][f][j] = live && d < a.D ? p[d * a.q_channel] : T(0.0f);
-        }
+        for (int j = 0; j < N; j++) v[j] = from[j * a.q_channel];
+        q[t][f] = d0 < a.D ? v : V{};
+      }
+    }
+    start();
+  }
+
+  __device__ __forceinline__ void start() {
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
 #pragma unroll
       for (int d = 0; d < DM; d++) o[d][t] = F4{0.0f, 0.0f, 0.0f, 0.0f};
       total[t] = F4{0.0f, 0.0f, 0.0f, 0.0f};
       top[t] = -kInf, use[t] = -kLift;
     }
+  }
+
+  // Whether a row that is there has a sum that is not finite.
+  __device__ __forceinline__ bool spoilt() const {
+    bool any = false;
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+      float none = 0.0f;
+#pragma unroll
+      for (int d = 0; d < DM; d++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) none = fmaf(o[d][t][i], 0.0f, none);
+      any |= pos[t] >= 0 && none != 0.0f;
+    }
+    return any;
   }
 
   // Whether every row sees all of keys k0 .. k0+31 (`miss`: halves of them that are on no page).
@@ -219,34 +248,46 @@ struct Rows {
 
   __device__ __forceinline__ float sum_of(int t) const { return kWide ? column_sum(total[t][0]) : total[t][0]; }
 
-  // o += the weights times the values, one key after another and only where a row sees it: 0 times infinity is
-  // no 0.  `w`: 16 x 33 floats of LDS for this wavefront; value(d, key).
+  // o += the weights times the values of a block that some rows see in part, with infinities or NaN among them: those only the rows that
+  // see them may meet (0 times infinity is no 0).  The finite values as always, and for the others two products of ones
+  // and zeros say which rows see a +infinity or NaN, and which a -infinity or NaN.  value(d, f): a lane's values.
+  // It takes so many registers that the walk over the context knows nothing of it: where a sum is not finite at
+  // its end (which is seldom), the walk is made again with it.
   template <class Value>
-  __device__ __forceinline__ void one_by_one(const F4 (&s)[2][NT], float* w, int k0, int miss, Value value) {
+  __device__ __forceinline__ void add_odd(const V (&p)[NT][VF], int k0, int miss, Value value) {
     int lanes = part;
     asm volatile("" : "+v"(lanes));  // keeps what is made of it out of the loop's registers
+    V seen[NT][VF];
 #pragma unroll
-    for (int t = 0; t < NT; t++) {
+    for (int t = 0; t < NT; t++)
 #pragma unroll
       for (int u = 0; u < 2; u++)
 #pragma unroll
-        for (int i = 0; i < 4; i++) w[col * 33 + key_of(lanes, u, i)] = hidden(lanes, k0, miss, u, t, i) ? -1.0f : s[u][t][i];
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-      for (int key = 0; key < kBlock; key++) {
-        const float weight = w[col * 33 + key];
+        for (int i = 0; i < 4; i++) seen[t][kWide ? u : 0][kWide ? i : 4 * u + i] = hidden(lanes, k0, miss, u, t, i) ? T(0.0f) : T(1.0f);
 #pragma unroll
-        for (int d = 0; d < DM; d++) {
-          F4 v = o[d][t];
+    for (int d = 0; d < DM; d++)
 #pragma unroll
-          for (int i = 0; i < 4; i++) v[i] = weight >= 0.0f ? fmaf(weight, value(d * 16 + 4 * lanes + i, key), v[i]) : v[i];
-          o[d][t] = v;
+      for (int f = 0; f < VF; f++) {
+        __builtin_amdgcn_sched_barrier(0);  // one after another: few registers
+        const W4 v = __builtin_bit_cast(W4, value(d, f));
+        W4 w, x, y;
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          const uint32_t odd = Bits<T>::spread(Bits<T>::full(v[j])), nan = Bits<T>::spread(Bits<T>::above_infinity(v[j])), neg = Bits<T>::spread(v[j]);
+          w[j] = v[j] & ~odd;
+          x[j] = odd & (nan | ~neg) & Bits<T>::kOnes;
+          y[j] = odd & (nan | neg) & Bits<T>::kOnes;
+        }
+        const V rest = __builtin_bit_cast(V, w), up = __builtin_bit_cast(V, x), down = __builtin_bit_cast(V, y);
+#pragma unroll
+        for (int t = 0; t < NT; t++) {
+          const F4 none = {0.0f, 0.0f, 0.0f, 0.0f}, ups = mma(up, seen[t][f], none), downs = mma(down, seen[t][f], none);
+          F4 odd;
+#pragma unroll
+          for (int i = 0; i < 4; i++) odd[i] = (ups[i] > 0.0f ? kInf : 0.0f) - (downs[i] > 0.0f ? kInf : 0.0f);
+          o[d][t] = mma(rest, p[t][f], o[d][t]) + odd;
         }
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-    }
   }
 };
 
@@ -281,7 +322,7 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
   constexpr int N = R::N, KF = R::KF, VF = R::VF, DM = R::DM;
   constexpr int kPitch = DT + 4;
   constexpr bool kAhead = DT * sizeof(T) < 1024;  // else a block's keys and values alone fill the registers
-  __shared__ float lds[4 * 16 * (kPitch > 33 ? kPitch : 33)];
+  __shared__ float lds[4 * 16 * kPitch];
   __shared__ float2 tops[4][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, part = lane >> 4;
   int id = xcd_logical(blockIdx.x, gridDim.x);
@@ -333,69 +374,65 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
     }
   };
 
-  int n = split * per + wave;
-  Where at, next;
-  if (n < stop) {
-    at = find(blocks.at(n));
-    if (kAhead) {
-      load_k(at);
-      load_v(at);
-    }
-  }
   R rows(a, r, b, g, row0, cut.pitch, lane);
-  for (; n < stop; n += 4) {
-    const int k0 = at.key, miss = (at.first < 0 ? 1 : 0) | (at.second < 0 ? 2 : 0);
-    const bool more = n + 4 < stop;
-    if (more) next = find(blocks.at(n + 4));
-    if (!kAhead) load_k(at);
-    F4 s[2][NT];
-#pragma unroll
-    for (int u = 0; u < 2; u++)
-#pragma unroll
-      for (int t = 0; t < NT; t++) {
-        s[u][t] = F4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int f = 0; f < KF; f++) s[u][t] = mma(kf[u][f], rows.q[t][f], s[u][t]);
+  auto walk = [&](auto odd) __attribute__((always_inline)) {
+    int n = split * per + wave;
+    Where at, next;
+    if (n < stop) {
+      at = find(blocks.at(n));
+      if (kAhead) {
+        load_k(at);
+        load_v(at);
       }
-    if (kAhead && more) load_k(next);
-    if (!kAhead) load_v(at);
-    const bool whole = rows.whole(k0, miss);
-    V p[NT][VF];
-    rows.weigh(s, p, k0, miss, whole);
-    bool odd = false;
-    if (!whole) {
-      // nothing that is not there reaches the product, and what only some rows see is looked at
-      uint32_t full = 0;
+    }
+    for (; n < stop; n += 4) {
+      const int k0 = at.key, miss = (at.first < 0 ? 1 : 0) | (at.second < 0 ? 2 : 0);
+      const bool more = n + 4 < stop;
+      if (more) next = find(blocks.at(n + 4));
+      if (!kAhead) load_k(at);
+      F4 s[2][NT];
 #pragma unroll
-      for (int f = 0; f < VF; f++) {
-        const int key = f * 4 * N + part * N, left = miss >> (key >> 4 & 1) & 1 ? 0 : r.end - k0 - key;
-        W4 keep;
+      for (int u = 0; u < 2; u++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) keep[j] = R::kWide ? (j < left ? ~0u : 0u) : (2 * j + 1 < left ? ~0u : 2 * j < left ? 0xffffu : 0u);
+        for (int t = 0; t < NT; t++) {
+          s[u][t] = F4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int d = 0; d < DM; d++) {
-          const W4 v = __builtin_bit_cast(W4, vf[d][f]) & keep;
-          vf[d][f] = __builtin_bit_cast(V, v);
+          for (int f = 0; f < KF; f++) s[u][t] = mma(kf[u][f], rows.q[t][f], s[u][t]);
+        }
+      if (kAhead && more) load_k(next);
+      if (!kAhead) load_v(at);
+      const bool whole = rows.whole(k0, miss);
+      V p[NT][VF];
+      rows.weigh(s, p, k0, miss, whole);
+      if (!whole) {  // nothing that is not there reaches the product
 #pragma unroll
-          for (int j = 0; j < 4; j++) full |= exponents_full<T>(v[j]);
+        for (int f = 0; f < VF; f++) {
+          const int key = f * 4 * N + part * N, left = miss >> (key >> 4 & 1) & 1 ? 0 : r.end - k0 - key;
+          W4 keep;
+#pragma unroll
+          for (int j = 0; j < 4; j++) keep[j] = R::kWide ? (j < left ? ~0u : 0u) : (2 * j + 1 < left ? ~0u : 2 * j < left ? 0xffffu : 0u);
+#pragma unroll
+          for (int d = 0; d < DM; d++) vf[d][f] = __builtin_bit_cast(V, __builtin_bit_cast(W4, vf[d][f]) & keep);
         }
       }
-      odd = any_full<T>(full);
+      if (odd && !whole) {
+        rows.add_odd(p, k0, miss, [&](int d, int f) { return vf[d][f]; });
+      } else {
+#pragma unroll
+        for (int f = 0; f < VF; f++)
+#pragma unroll
+          for (int d = 0; d < DM; d++)
+#pragma unroll
+            for (int t = 0; t < NT; t++) rows.o[d][t] = mma(vf[d][f], p[t][f], rows.o[d][t]);
+      }
+      if (kAhead && more) load_v(next);
+      at = next;
     }
-    if (__builtin_expect(odd, false)) {
-      rows.one_by_one(s, lds + wave * (16 * 33), k0, miss, [&](int d, int key) {
-        return k0 + key < r.end ? (float)value_at(at, key)[min(d, a.D - 1) * a.P] : 0.0f;
-      });
-    } else {
-#pragma unroll
-      for (int f = 0; f < VF; f++)
-#pragma unroll
-        for (int d = 0; d < DM; d++)
-#pragma unroll
-          for (int t = 0; t < NT; t++) rows.o[d][t] = mma(vf[d][f], p[t][f], rows.o[d][t]);
-    }
-    if (kAhead && more) load_v(next);
-    at = next;
+  };
+  walk(std::false_type());
+  if (__builtin_expect(__any(rows.spoilt()), false)) {
+    rows.start();
+    walk(std::true_type());
   }
 
   // the four wavefronts' sums, 16 rows at a time
@@ -450,15 +487,28 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
 // 16-byte pieces are dealt out by an exclusive or with the row, so that the sixteen rows that a read takes
 // lie in sixteen different places of 256 bytes.
 
-// 16 bytes a lane from its address to LDS byte address `to` + 16 * lane (to: the same in all lanes).  Written
-// as asm so that the compiler does not wait for it before every LDS read; the wait is at the tile's end.
+// 16 bytes a lane, from its address or from a base that the lanes share and a byte offset of its own, to LDS byte address
+// `to` + 16 * lane (to: the same in all lanes).  Written as asm so that the compiler does not wait for it
+// before every LDS read; the wait is at the tile's end.
 __device__ __forceinline__ void to_lds(uint32_t to, const void* from) {
   asm volatile(
       "s_mov_b32 m0, %0\n\t"
       "s_nop 0\n\t"
       "global_load_lds_dwordx4 %1, off"
       :
-      : "s"(to), "v"(from)
+      : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(from)
+      : "memory", "m0");
+}
+__device__ __forceinline__ void to_lds(uint32_t to, const void* base, uint32_t offset) {
+  const uint64_t at = (uint64_t)base;
+  const uint64_t shared = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32)) << 32 |
+                          (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at);
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, %2"
+      :
+      : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(offset), "s"(shared)
       : "memory", "m0");
 }
 
@@ -476,7 +526,8 @@ struct Stage {
   static __device__ __forceinline__ int value_piece(int d, int c) { return c ^ (CV >= 16 ? d & 15 : CV == 8 ? d >> 1 & 7 : d >> 2 & 3); }
 };
 
-template <class T, int DT, int NT>
+// EXACT: D is DT.
+template <class T, int DT, int NT, bool EXACT>
 __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2) void attend_staged(const sc_paged_attention a, const Cut cut) {
   typedef Rows<T, DT, NT> R;
   typedef Stage<T, DT> S;
@@ -484,7 +535,7 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
   constexpr int N = R::N, KF = R::KF, VF = R::VF, DM = R::DM, KT = S::KT;
   constexpr int KI = S::kKeys / 4096;                      // copies of a wavefront's for the keys, and as many for the values
   constexpr int RK = 64 / S::CK, RV = 64 / S::CV;          // rows of one copy
-  __shared__ __align__(256) char lds[2 * S::kBytes + 4 * 16 * 33 * 4];
+  __shared__ __align__(256) char lds[2 * S::kBytes];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, part = lane >> 4;
   // the rows that see most come first, and a head of keys stays on its XCDs
   const int heads = a.B * a.G, share = a.H / a.G;
@@ -510,8 +561,8 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
   const int vc = S::value_piece(RV * wave + vr, lane % S::CV) * N;  // the same for every i
   const T* k_head = static_cast<const T*>(a.k_pages) + (int64_t)g * a.P * a.D;
   const T* v_head = static_cast<const T*>(a.v_pages) + (int64_t)g * a.P * a.D;
-  // which sixteens of the tile's keys are on no page
-  auto copy = [&](int k0, int buffer) {
+  // copies a tile; returns which sixteens of its keys are on no page
+  auto copy = [&](int k0, int buffer) __attribute__((always_inline)) {
     int page[KT / 16], miss = 0;
 #pragma unroll
     for (int h = 0; h < KT / 16; h++) {
@@ -521,111 +572,107 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
     const uint32_t to = base + buffer * S::kBytes + wave * 1024;
 #pragma unroll
     for (int i = 0; i < KI; i++) {
-      const int first = RK * (4 * i + wave), key = first + kr, c = S::key_piece(key, kc) * N;
+      const int first = RK * (4 * i + wave), c = S::key_piece(first + kr, kc) * N;
       int pg = page[0];
 #pragma unroll
       for (int h = 1; h < KT / 16; h++) pg = first >> 4 == h ? page[h] : pg;
-      const T* from = k_head + pg * a.k_page + ((k0 + key) & (a.P - 1)) * a.D + c;
-      if (DT == 64 || a.D == DT || c < a.D) {
-        if (c < a.D) to_lds(to + i * 4096, from);
-      }
+      const T* from = k_head + pg * a.k_page + ((k0 + first) & (a.P - 1)) * a.D;  // its RK keys are one page's
+      if (EXACT || c < a.D) to_lds(to + i * 4096, from, (kr * a.D + c) * (int)sizeof(T));
     }
-    int pg = page[0];
+    if (a.P >= KT) {
+      const T* from = v_head + page[0] * a.v_page + (k0 & (a.P - 1));
 #pragma unroll
-    for (int h = 1; h < KT / 16; h++) pg = vc >> 4 == h ? page[h] : pg;
-    const T* from = v_head + pg * a.v_page + ((k0 + vc) & (a.P - 1));
+      for (int i = 0; i < KI; i++) {
+        const int first = RV * (4 * i + wave);
+        if (EXACT || first + vr < a.D) to_lds(to + S::kKeys + i * 4096, from + first * a.P, (vr * a.P + vc) * (int)sizeof(T));
+      }
+    } else {
+      int pg = page[0];
 #pragma unroll
-    for (int i = 0; i < KI; i++) {
-      const int d = RV * (4 * i + wave) + vr;
-      if (d < a.D) to_lds(to + S::kKeys + i * 4096, from + d * a.P);
+      for (int h = 1; h < KT / 16; h++) pg = vc >> 4 == h ? page[h] : pg;
+      const T* from = v_head + pg * a.v_page + ((k0 + vc) & (a.P - 1)) + vr * a.P;
+#pragma unroll
+      for (int i = 0; i < KI; i++) {
+        const int first = RV * (4 * i + wave);
+        if (EXACT || first + vr < a.D) to_lds(to + S::kKeys + i * 4096, from + first * a.P);
+      }
     }
     return miss;
   };
-  int n = split * per, miss = 0, k0 = tiles.at(n) * KT;
-  if (a.D != DT) {  // dims past D are never copied: both products take them as 0
+  if (!EXACT) {  // dims past D are never copied: both products take them as 0
     for (int e = threadIdx.x; e < 2 * S::kBytes / 16; e += 256) reinterpret_cast<W4*>(lds)[e] = W4{0, 0, 0, 0};
     __syncthreads();
   }
-  if (n < stop) miss = copy(k0, 0);
-  R rows(a, r, b, g, row0, cut.pitch, lane);
-  // the rows' own part of the tile's keys
+  // the rows' own part of the tiles' keys
   const int until = r.any ? max(min(r.past + r.last + 1, r.end), r.prefix) : 0;
   const int from = r.any && a.window ? r.past + r.first - a.window + 1 : 0;
-  int buffer = 0;
-  for (; n < stop; n++, buffer ^= 1) {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");  // this tile is there, and nobody reads the one before
-    const int here = k0, gone = miss;
-    if (n + 1 < stop) {
-      k0 = tiles.at(n + 1) * KT;
-      miss = copy(k0, buffer ^ 1);
-    }
-    char* keys = lds + buffer * S::kBytes;
-    char* values = keys + S::kKeys;
-    if (here + KT > r.end || gone) {  // nothing that is not there reaches the product
-      for (int e = threadIdx.x; e < S::kKeys / 16; e += 256) {
-        const int d = e / S::CV, key = S::value_piece(d, e % S::CV) * N, left = gone >> (key >> 4) & 1 ? 0 : r.end - here - key;
-        if (left >= N) continue;
-        W4 v = reinterpret_cast<W4*>(values)[e];
-#pragma unroll
-        for (int j = 0; j < 4; j++) v[j] &= R::kWide ? (j < left ? ~0u : 0u) : (2 * j + 1 < left ? ~0u : 2 * j < left ? 0xffffu : 0u);
-        reinterpret_cast<W4*>(values)[e] = v;
+  R rows(a, r, b, g, row0, cut.pitch, lane);
+  auto walk = [&](auto odd) __attribute__((always_inline)) {
+    int n = split * per, miss = 0, k0 = tiles.at(n) * KT, buffer = 0;
+    if (n < stop) miss = copy(k0, 0);
+    for (; n < stop; n++, buffer ^= 1) {
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");  // this tile is there, and nobody reads the one before
+      const int here = k0, gone = miss;
+      if (n + 1 < stop) {
+        k0 = tiles.at(n + 1) * KT;
+        miss = copy(k0, buffer ^ 1);
       }
-      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    }
+      char* keys = lds + buffer * S::kBytes;
+      char* values = keys + S::kKeys;
+      if (here + KT > r.end || gone) {  // nothing that is not there reaches the product
+        for (int e = threadIdx.x; e < S::kKeys / 16; e += 256) {
+          const int d = e / S::CV, key = S::value_piece(d, e % S::CV) * N, left = gone >> (key >> 4) & 1 ? 0 : r.end - here - key;
+          if (left >= N) continue;
+          W4 v = reinterpret_cast<W4*>(values)[e];
 #pragma unroll
-    for (int kb = 0; kb < KT / kBlock; kb++) {
-      const int at = here + kb * kBlock, lost = gone >> (2 * kb) & 3;
-      if (at >= until || (at + kBlock <= from && at >= r.prefix)) continue;
-      F4 s[2][NT];
+          for (int j = 0; j < 4; j++) v[j] &= R::kWide ? (j < left ? ~0u : 0u) : (2 * j + 1 < left ? ~0u : 2 * j < left ? 0xffffu : 0u);
+          reinterpret_cast<W4*>(values)[e] = v;
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      }
 #pragma unroll
-      for (int u = 0; u < 2; u++) {
-        const int key = kb * kBlock + R::key_row(u, col);
-        V kf[KF];
+      for (int kb = 0; kb < KT / kBlock; kb++) {
+        const int at = here + kb * kBlock, lost = gone >> (2 * kb) & 3;
+        if (at >= until || (at + kBlock <= from && at >= r.prefix)) continue;
+        F4 s[2][NT];
 #pragma unroll
-        for (int f = 0; f < KF; f++) kf[f] = *reinterpret_cast<const V*>(keys + key * S::kKeyRow + S::key_piece(key, 4 * f + part) * 16);
+        for (int u = 0; u < 2; u++) {
+          const int key = kb * kBlock + R::key_row(u, col);
+          V kf[KF];
 #pragma unroll
-        for (int t = 0; t < NT; t++) {
-          s[u][t] = F4{0.0f, 0.0f, 0.0f, 0.0f};
+          for (int f = 0; f < KF; f++) kf[f] = *reinterpret_cast<const V*>(keys + key * S::kKeyRow + S::key_piece(key, 4 * f + part) * 16);
 #pragma unroll
-          for (int f = 0; f < KF; f++) s[u][t] = mma(kf[f], rows.q[t][f], s[u][t]);
+          for (int t = 0; t < NT; t++) {
+            s[u][t] = F4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int f = 0; f < KF; f++) s[u][t] = mma(kf[f], rows.q[t][f], s[u][t]);
+          }
+        }
+        const bool whole = rows.whole(at, lost);
+        V p[NT][VF];
+        rows.weigh(s, p, at, lost, whole);
+        auto value = [&](int d, int f) {
+          return *reinterpret_cast<const V*>(values + (d * 16 + col) * S::kValueRow + S::value_piece(d * 16 + col, (kb * VF + f) * 4 + part) * 16);
+        };
+        if (odd && !whole) {
+          rows.add_odd(p, at, lost, value);
+        } else {
+#pragma unroll
+          for (int f = 0; f < VF; f++)
+#pragma unroll
+            for (int d = 0; d < DM; d++) {
+              const V v = value(d, f);
+#pragma unroll
+              for (int t = 0; t < NT; t++) rows.o[d][t] = mma(v, p[t][f], rows.o[d][t]);
+            }
         }
       }
-      const bool whole = rows.whole(at, lost);
-      V p[NT][VF];
-      rows.weigh(s, p, at, lost, whole);
-      auto value = [&](int d, int f) {
-        return *reinterpret_cast<const V*>(values + d * S::kValueRow + S::value_piece(d, (kb * VF + f) * 4 + part) * 16);
-      };
-      bool odd = false;
-      if (!whole) {
-        uint32_t full = 0;
-#pragma unroll
-        for (int f = 0; f < VF; f++)
-#pragma unroll
-          for (int d = 0; d < DM; d++) {
-            const W4 v = __builtin_bit_cast(W4, value(d * 16 + col, f));
-#pragma unroll
-            for (int j = 0; j < 4; j++) full |= exponents_full<T>(v[j]);
-          }
-        odd = any_full<T>(full);
-      }
-      if (__builtin_expect(odd, false)) {
-        float* w = reinterpret_cast<float*>(lds + 2 * S::kBytes) + wave * (16 * 33);
-        rows.one_by_one(s, w, at, lost, [&](int d, int key) {
-          const int k = kb * kBlock + key;
-          return (float)*reinterpret_cast<const T*>(values + d * S::kValueRow + S::value_piece(d, k / N) * 16 + k % N * sizeof(T));
-        });
-      } else {
-#pragma unroll
-        for (int f = 0; f < VF; f++)
-#pragma unroll
-          for (int d = 0; d < DM; d++) {
-            const V v = value(d * 16 + col, f);
-#pragma unroll
-            for (int t = 0; t < NT; t++) rows.o[d][t] = mma(v, p[t][f], rows.o[d][t]);
-          }
-      }
     }
+  };
+  walk(std::false_type());
+  if (__builtin_expect(__builtin_amdgcn_readfirstlane(__syncthreads_or(rows.spoilt())), false)) {
+    rows.start();
+    walk(std::true_type());
   }
 
 #pragma unroll
@@ -639,7 +686,7 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
       if (part == 0) cut.tops[at] = make_float2(none ? -kInf : rows.top[t], none ? 0.0f : total);
 #pragma unroll
       for (int d = 0; d < DM; d++)
-        if (d * 16 + part * 4 < a.D) *reinterpret_cast<F4*>(cut.sums + at * a.D + d * 16 + part * 4) = rows.o[d][t];
+        if (EXACT || d * 16 + part * 4 < a.D) *reinterpret_cast<F4*>(cut.sums + at * a.D + d * 16 + part * 4) = rows.o[d][t];
     } else {
       const float by = none ? 0.0f : 1.0f / total;
       const int64_t out = b * a.out_batch + (int64_t)(g * share + h) * a.D * a.out_channel + i;
@@ -648,7 +695,7 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
 #pragma unroll
         for (int j = 0; j < 4; j++) {
           const int dim = d * 16 + part * 4 + j;
-          if (dim >= a.D) continue;
+          if (!EXACT && dim >= a.D) continue;
           const float v = none ? 0.0f : rows.o[d][t][j] * by;
           if (a.flags & SC_ATT_OUT_F32)
             static_cast<float*>(a.out)[out + dim * a.out_channel] = v;
@@ -706,7 +753,10 @@ int launch_direct(const sc_paged_attention& a, const AttendPlan& p, const Cut& c
 template <class T, int DT, int NT>
 int launch_staged(const sc_paged_attention& a, const AttendPlan& p, const Cut& cut, hipStream_t st) {
   const int64_t blocks = (int64_t)a.B * a.G * p.groups();
-  hipLaunchKernelGGL((attend_staged<T, DT, NT>), dim3((unsigned)blocks), dim3(256), 0, st, a, cut);
+  if (a.D == DT)
+    hipLaunchKernelGGL((attend_staged<T, DT, NT, true>), dim3((unsigned)blocks), dim3(256), 0, st, a, cut);
+  else
+    hipLaunchKernelGGL((attend_staged<T, DT, NT, false>), dim3((unsigned)blocks), dim3(256), 0, st, a, cut);
   return (int)hipGetLastError();
 }
 
