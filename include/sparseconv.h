@@ -655,7 +655,7 @@ typedef struct {
  *     norm(v) = (v - m) / sqrt(mean((v - m)^2) + eps),  m = mean(v) with SC_NORM_CENTER, else 0,
  *     post(v) = norm(v) * post_weight + post_bias where there is a post_weight, else v.
  * r is normed before it is rounded.  "x itself": the same pointer and strides.  B, L >= 0, C >= 1.
- * Limits: C < 2^20, L < 2^30, B*ceil(L/8) < 2^22.
+ * Limits: C < 2^20, L < 2^30, B*ceil(L/4) < 2^22.
  */
 sc_status sparseconv_residual_norm(const sc_residual_norm* a, void* hip_stream);
 

@@ -170,7 +170,7 @@ sc_status sparseconv_residual_norm(const sc_residual_norm* a, void* hip_stream) 
     if (bad_dtype(a->dtype)) return fail(SC_EINVAL, "unknown dtype");
     if ((a->flags & ~SC_NORM_CENTER) || a->reserved) return fail(SC_EINVAL, "unknown flag, or reserved is not 0");
     if (a->B < 0 || a->L < 0 || a->C < 1) return fail(SC_ESHAPE, "B, L >= 0 and C >= 1");
-    if (a->C >= (1 << 20) || a->L >= (1 << 30) || !sc::norm_fits(*a)) return fail(SC_EUNSUPPORTED, "C >= 2^20, L >= 2^30 or B*ceil(L/8) >= 2^22");
+    if (a->C >= (1 << 20) || a->L >= (1 << 30) || !sc::norm_fits(*a)) return fail(SC_EUNSUPPORTED, "C >= 2^20, L >= 2^30 or B*ceil(L/4) >= 2^22");
     if (a->B == 0 || a->L == 0) return SC_OK;
     const int64_t es = size_of(a->dtype);
     if (!a->x || (!a->sum && !a->out)) return fail(SC_EINVAL, "x, or both of sum and out, is NULL");

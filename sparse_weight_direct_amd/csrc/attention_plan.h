@@ -96,7 +96,50 @@ inline bool copy_fits(const sc_cache_copy& a) {
   return pieces < kMostGroups && (int64_t)a.outer * a.count < kMostGroups && a.outer * pieces * a.count < kMostGroups;
 }
 
-// ---- Norm: tiles of at least 8 positions
-inline bool norm_fits(const sc_residual_norm& a) { return a.B * ceil_div(a.L, 8) < (1LL << 22); }
+// ---- Norm
+enum NormForm { kNormAny, kNormPrompt, kNormToken };
+
+// Prompts.  Measured, us (16-bit, or fp32 where it says so; lanes side by side, channels a thread, threads):
+//
+//   8 x 2048 x 2048       4,16,512: 79.7   2,8,512: 129    1,4,512: 124    2,16,256: 115   4,8,1024: 97
+//   8 x 1024 x 2048       4,8,512: 44.7    2,4,512: 37.4   4,16,256: 34.5  2,8,256: 57.9
+//   4 x 4096 x 2048       2,16,512: 107    1,8,512: 135    1,16,256: 127   2,8,1024: 111
+//   1 x 1024 x 512        4,8,512: 17.2    2,4,512: 11.1   4,16,256: 19.6  2,8,256: 15.3
+//   4 x 1024 x 512, fp32  4,8,512: 15.1    2,4,512: 13.6   4,16,256: 18.0
+//
+// so four lanes (64 bytes of a row) and as few threads as hold the channels, where every CU has two tiles, else two lanes.
+struct NormPlan {
+  NormForm form;
+  int tiles;     // of a sequence's positions
+  int lp_shift;  // prompts: log2 of the lanes side by side along the positions, 16 bytes each
+  int pass;      // prompts: channels of a thread
+  int threads;
+};
+
+inline NormPlan norm_plan(const sc_residual_norm& a, int cus) {
+  NormPlan p{kNormAny, (int)ceil_div(a.L, 16), 0, 0, 256};
+  const bool rows = (!a.y || a.y_channel == 1) && (!a.sum || a.sum_channel == 1) && (!a.out || a.out_channel == 1) && a.x_channel == 1;
+  if (a.L == 1 && rows && a.C <= 8192) {
+    p.form = kNormToken;
+    p.threads = a.C <= 2048 ? 256 : a.C <= 4096 ? 512 : 1024;
+    return p;
+  }
+  const int V = a.dtype == SC_F32 ? 4 : 8;
+  const bool many = a.B * ceil_div(a.L, 4 * V) >= 2 * cus;
+  for (int shift = many ? 2 : 1; shift >= 0; shift--)
+    for (int threads = many ? 256 : 512; threads <= 512; threads *= 2) {
+      const int64_t need = ceil_div(a.C, threads >> shift);
+      if (need > 16) continue;
+      p.form = kNormPrompt;
+      p.lp_shift = shift, p.threads = threads;
+      p.tiles = (int)ceil_div(a.L, V << shift);
+      p.pass = need <= 4 ? 4 : need <= 8 ? 8 : 16;
+      return p;
+    }
+  return p;
+}
+
+// Tiles of at least 4 positions, of at most 1024 threads.
+inline bool norm_fits(const sc_residual_norm& a) { return a.B * ceil_div(a.L, 4) < (1LL << 22); }
 
 }  // namespace sc
