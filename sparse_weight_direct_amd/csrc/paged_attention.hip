@@ -130,8 +130,14 @@ struct Rows {
         const int d0 = f * 4 * N + part * N;  // D is a multiple of N: all N dims are there or none
         const T* from = p + min(d0, a.D - N) * a.q_channel;
         V v;
+        if (a.q_channel == 1) {  // single positions
+          const typename Pack<T, N>::type w = *reinterpret_cast<const typename Pack<T, N>::type*>(from);
 #pragma unroll
-        for (int j = 0; j < N; j++) v[j] = from[j * a.q_channel];
+          for (int j = 0; j < N; j++) v[j] = w[j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < N; j++) v[j] = from[j * a.q_channel];
+        }
         q[t][f] = d0 < a.D ? v : V{};
       }
     }
@@ -304,6 +310,26 @@ struct Blocks {
   __device__ __forceinline__ int at(int n) const { return n < prefix ? n : n + jump; }
 };
 
+// Four dims of a row of the output.
+template <class T>
+__device__ __forceinline__ void put4(const sc_paged_attention& a, int64_t at, F4 v) {
+  if (a.flags & SC_ATT_OUT_F32) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) static_cast<float*>(a.out)[at + i * a.out_channel] = v[i];
+    return;
+  }
+  T* out = static_cast<T*>(a.out) + at;
+  if (a.out_channel == 1) {
+    typename Pack<T, 4>::type w;
+#pragma unroll
+    for (int i = 0; i < 4; i++) w[i] = T(v[i]);
+    *reinterpret_cast<typename Pack<T, 4>::type*>(out) = w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; i++) out[i * a.out_channel] = T(v[i]);
+  }
+}
+
 // Page `at` of a sequence's table, negative where there is none.
 __device__ __forceinline__ int page_of(const sc_paged_attention& a, const int32_t* table, int at) {
   const int p = at < a.width ? table[at] : -1;
@@ -316,7 +342,7 @@ __device__ __forceinline__ int page_of(const sc_paged_attention& a, const int32_
 // blocks in turn, operands straight from the cache to registers (each byte is read once), the next block's on their
 // way while one is computed, and their sums are joined at the end.
 template <class T, int DT, int NT>
-__global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2) void attend_direct(const sc_paged_attention a, const Cut cut) {
+__global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : NT > 1 || (DT == 128 && sizeof(T) == 2) ? 2 : 3) void attend_direct(const sc_paged_attention a, const Cut cut) {
   typedef Rows<T, DT, NT> R;
   typedef typename R::V V;
   constexpr int N = R::N, KF = R::KF, VF = R::VF, DM = R::DM;
@@ -325,9 +351,9 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
   __shared__ float lds[4 * 16 * kPitch];
   __shared__ float2 tops[4][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, part = lane >> 4;
-  int id = xcd_logical(blockIdx.x, gridDim.x);
-  const int split = id % cut.splits;
-  id /= cut.splits;
+  // the pieces one after another: those that have no blocks would else leave whole groups of CUs idle
+  const int each = gridDim.x / cut.splits, split = blockIdx.x / each;
+  int id = xcd_logical(blockIdx.x % each, each);
   const int tile = id % cut.tiles;
   id /= cut.tiles;
   const int g = id % a.G, b = id / a.G, share = a.H / a.G, row0 = tile * 16 * NT;
@@ -341,17 +367,17 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
     int first, second, key;
   };
   const int32_t* table = a.table + b * a.table_batch;
-  auto find = [&](int blk) {
+  auto find = [&](int blk) __attribute__((always_inline)) {
     return Where{page_of(a, table, blk * kBlock >> shift), page_of(a, table, (blk * kBlock + 16) >> shift), blk * kBlock};
   };
   // of key `key` of the block: its dims, and its values of dim 0
   const T* k_head = static_cast<const T*>(a.k_pages) + (int64_t)g * a.P * a.D;
   const T* v_head = static_cast<const T*>(a.v_pages) + (int64_t)g * a.P * a.D;
-  auto page_at = [&](Where w, int key) { return max(key & 16 ? w.second : w.first, 0); };
-  auto key_at = [&](Where w, int key) { return k_head + page_at(w, key) * a.k_page + ((w.key + key) & (a.P - 1)) * a.D; };
-  auto value_at = [&](Where w, int key) { return v_head + page_at(w, key) * a.v_page + ((w.key + key) & (a.P - 1)); };
+  auto page_at = [&](Where w, int key) __attribute__((always_inline)) { return max(key & 16 ? w.second : w.first, 0); };
+  auto key_at = [&](Where w, int key) __attribute__((always_inline)) { return k_head + page_at(w, key) * a.k_page + ((w.key + key) & (a.P - 1)) * a.D; };
+  auto value_at = [&](Where w, int key) __attribute__((always_inline)) { return v_head + page_at(w, key) * a.v_page + ((w.key + key) & (a.P - 1)); };
   V kf[2][KF], vf[DM][VF];
-  auto load_k = [&](Where w) {
+  auto load_k = [&](Where w) __attribute__((always_inline)) {
 #pragma unroll
     for (int t = 0; t < 2; t++) {
       const T* p = key_at(w, R::key_row(t, col));
@@ -365,7 +391,7 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
         for (int f = 0; f < KF; f++)
           kf[t][f] = f * 4 * N + part * N < a.D ? kf[t][f] : V{};
   };
-  auto load_v = [&](Where w) {
+  auto load_v = [&](Where w) __attribute__((always_inline)) {
 #pragma unroll
     for (int f = 0; f < VF; f++) {
       const T* p = value_at(w, f * 4 * N + part * N);
@@ -461,21 +487,25 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
     for (int w = 0; w < 4; w++) none = none & (tops[w][row].y == 0.0f);
     none = none | (i >= r.len);  // (where whole blocks are seen, rows that are not there saw them too)
     const int64_t ws_row = ((int64_t)(b * a.G + g) * cut.tiles + tile) * (16 * NT) + t * 16 + row;
-    const float by = cut.splits > 1 ? 1.0f : none ? 0.0f : seen ? 1.0f / l : __builtin_nanf("");
-    if (cut.splits > 1 && piece == 0)
-      cut.tops[ws_row * cut.splits + split] = make_float2(none ? -kInf : m, none ? 0.0f : seen ? l : __builtin_nanf(""));
+    const float by = none ? 0.0f : cut.splits > 1 ? 1.0f : seen ? 1.0f / l : __builtin_nanf("");
+    const int64_t ws = ws_row * cut.splits + split;
+    if (cut.splits > 1 && piece == 0) cut.tops[ws] = make_float2(none ? -kInf : m, none ? 0.0f : seen ? l : __builtin_nanf(""));
     const int64_t out = b * a.out_batch + (int64_t)(g * share + h) * a.D * a.out_channel + i;
-    for (int d = piece * (DT / 16); d < min((piece + 1) * (DT / 16), a.D); d++) {
-      float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < 4; w++) v += f[w] != 0.0f ? f[w] * lds[(w * 16 + row) * kPitch + d] : 0.0f;
-      v = none ? 0.0f : v * by;
+    for (int k = 0; k < DT / 64; k++) {  // four dims at a time, pieces side by side
+      const int d = (k * 16 + piece) * 4;
+      if (d >= a.D) continue;
+      F4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int w = 0; w < 4; w++) {
+        const F4 u = *reinterpret_cast<const F4*>(&lds[(w * 16 + row) * kPitch + d]) * f[w];
+        v += f[w] != 0.0f ? u : F4{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+      v = none ? F4{0.0f, 0.0f, 0.0f, 0.0f} : v * by;
       if (cut.splits > 1)
-        cut.sums[(ws_row * cut.splits + split) * a.D + d] = v;
-      else if (a.flags & SC_ATT_OUT_F32)
-        static_cast<float*>(a.out)[out + d * a.out_channel] = v;
+        *reinterpret_cast<F4*>(cut.sums + ws * a.D + d) = v;
       else
-        static_cast<T*>(a.out)[out + d * a.out_channel] = T(v);
+        put4<T>(a, out + d * a.out_channel, v);
     }
   }
 }
@@ -706,40 +736,53 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
   }
 }
 
-// The pieces of the context, joined: a wavefront has a row.
-template <class T>
+// The pieces of the context, joined.  A workgroup has R rows, 16 threads a row with four dims each, and 16 / R threads for
+// every R-th of the pieces: with 16 rows what neighbours store lies side by side, positions in prompts and dims of single
+// positions; many pieces of few rows take the other form.  Four pieces' loads are in flight, none behind a
+// branch (a piece that saw nothing has no sums: what is read there is dropped).
+template <class T, int R>
 __global__ __launch_bounds__(256) void attend_join(const sc_paged_attention a, const Cut cut, int rows) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int64_t per = (int64_t)cut.tiles * rows;  // of a head of keys
-  const int g = row / per % a.G, b = row / per / a.G, share = a.H / a.G;
-  if (b >= a.B) return;
-  const int at = row % per, h = at / cut.pitch, i = at - h * cut.pitch;
-  if (h >= share || i >= a.L) return;
+  constexpr int SG = 16 / R;
+  __shared__ F4 part[SG > 1 ? SG : 1][R][16];
+  __shared__ float totals[SG > 1 ? SG : 1][R][16];
+  const int mine = threadIdx.x % R, piece = threadIdx.x / R & 15, sg = threadIdx.x / (16 * R);
+  const int64_t row = (int64_t)blockIdx.x * R + mine, per = (int64_t)cut.tiles * rows;  // rows of a head of keys
+  const int bg = row / per, b = bg / a.G, g = bg % a.G, share = a.H / a.G;
+  const int at = (int)(row % per), h = at / cut.pitch, i = at - h * cut.pitch;
+  const bool there = h < share && i < a.L;
   const float2* tops = cut.tops + row * cut.splits;
-  float m = -kInf, l = 0.0f;
-  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s = 0; s < cut.splits; s++) m = fmaxf(m, tops[s].x);
-  for (int s = 0; s < cut.splits; s++) {
-    const float2 e = tops[s];
-    if (e.y == 0.0f) continue;
-    const float f = e.x == -kInf ? 1.0f : exp2_fast(e.x - m);  // without a maximum: NaN
-    l += f * e.y;
-    const float* p = cut.sums + (row * cut.splits + s) * a.D;
-#pragma unroll
-    for (int k = 0; k < 4; k++)
-      if (lane + 64 * k < a.D) v[k] += f * p[lane + 64 * k];
-  }
-  const float by = l == 0.0f ? 0.0f : 1.0f / l;
+  float m = -kInf;
+  if (there)
+#pragma unroll 4
+    for (int s = 0; s < cut.splits; s++) m = fmaxf(m, tops[s].x);
   const int64_t out = b * a.out_batch + (int64_t)(g * share + h) * a.D * a.out_channel + i;
+  for (int d0 = 0; d0 < a.D; d0 += 64) {
+    const int d = d0 + piece * 4;
+    F4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    float l = 0.0f;
+    if (there && d < a.D) {
+      const float* sums = cut.sums + row * cut.splits * a.D + d;
+#pragma unroll 4
+      for (int s = sg; s < cut.splits; s += SG) {
+        const float2 e = tops[s];
+        const F4 p = *reinterpret_cast<const F4*>(sums + (int64_t)s * a.D);
+        const bool none = e.y == 0.0f;
+        const float f = none ? 0.0f : e.x == -kInf ? 1.0f : exp2_fast(e.x - m);  // without a maximum: NaN
+        l += f * e.y;
+        const F4 w = p * f;
+        v += none ? F4{0.0f, 0.0f, 0.0f, 0.0f} : w;
+      }
+    }
+    if (SG > 1) {
+      if (d0) __syncthreads();
+      part[sg][mine][piece] = v;
+      totals[sg][mine][piece] = l;
+      __syncthreads();
+      if (sg) continue;
 #pragma unroll
-  for (int k = 0; k < 4; k++) {
-    const int d = lane + 64 * k;
-    if (d >= a.D) continue;
-    if (a.flags & SC_ATT_OUT_F32)
-      static_cast<float*>(a.out)[out + d * a.out_channel] = v[k] * by;
-    else
-      static_cast<T*>(a.out)[out + d * a.out_channel] = T(v[k] * by);
+      for (int k = 1; k < SG; k++) v += part[k][mine][piece], l += totals[k][mine][piece];
+    }
+    if (there && d < a.D) put4<T>(a, out + d * a.out_channel, l == 0.0f ? F4{0.0f, 0.0f, 0.0f, 0.0f} : v * (1.0f / l));
   }
 }
 
@@ -782,7 +825,10 @@ int launch_type(const sc_paged_attention& a, int cus, hipStream_t st) {
   }
   const int e = a.D <= 64 ? launch_dims<T, 64>(a, p, cut, st) : a.D <= 128 ? launch_dims<T, 128>(a, p, cut, st) : launch_dims<T, 256>(a, p, cut, st);
   if (e || p.splits == 1) return e;
-  hipLaunchKernelGGL(attend_join<T>, dim3((unsigned)ceil_div(rows, 4)), dim3(256), 0, st, a, cut, p.rows());
+  if (p.splits > 8 && rows < 64 * cus)
+    hipLaunchKernelGGL((attend_join<T, 2>), dim3((unsigned)(rows / 2)), dim3(256), 0, st, a, cut, p.rows());
+  else
+    hipLaunchKernelGGL((attend_join<T, 16>), dim3((unsigned)(rows / 16)), dim3(256), 0, st, a, cut, p.rows());
   return (int)hipGetLastError();
 }
 
