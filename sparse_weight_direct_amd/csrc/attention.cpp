@@ -141,7 +141,7 @@ sc_status sparseconv_cache_append(const sc_cache_append* a, void* hip_stream) {
       if (overlap(i, kp) || overlap(i, vp) || (!(in_place && i.p == q.p && &i == in) && overlap(i, q_out)))
         return fail(SC_EINVAL, "an output overlaps an input");
     if (overlap(q_out, kp) || overlap(q_out, vp)) return fail(SC_EINVAL, "q_out and the cache overlap");
-    return launched(sc::launch_cache_append(*a, hip_stream));
+    return launched(sc::launch_cache_append(*a, device_cus(), hip_stream));
   });
 }
 

@@ -74,16 +74,19 @@ inline bool attend_fits(const sc_paged_attention& a) {
 
 // ---- Append
 constexpr int kAppendTile = 64;  // positions of a prompt's tile, whole in the cache: a thread's 8 lie in one page
-constexpr int kAppendHeads = 8;  // heads of a workgroup
 
+// Heads of a workgroup: their sines and cosines are made once.  Measured with 1, 2, 4, 8, 12 of them, us, 32 heads of q over 8 of
+// 128 dims, bf16: 2 x 4096 positions 111, 91, 77, 64.5, 66.6; 1 x 512: 12.2, 12.2, 18.5, 30.4, 29.3; 1 x 17: 8.3, 11.1,
+// 17.7, 30.4, 36.4; 16 over 16 of 64 dims, 4 x 1000: 20.8, 18.5, 19.1, 26.1, 31.3.  So as many, up to 8, as leave three workgroups a CU.
 struct AppendPlan {
+  int chunk;
   bool few;                        // a thread for every pair of every position
   int tiles, turners, sharers;     // else: tiles of a sequence (one more than its length needs, where the past ends
                                    // inside one); workgroups of a tile that turn q and k, and that move v
   int64_t groups;
 };
 
-inline AppendPlan append_plan(const sc_cache_append& a) {
+inline AppendPlan append_plan(const sc_cache_append& a, int cus) {
   AppendPlan p{};
   const int64_t heads = a.q ? a.H : 0;
   p.few = a.L < 16;
@@ -91,8 +94,11 @@ inline AppendPlan append_plan(const sc_cache_append& a) {
     p.groups = ceil_div((int64_t)a.B * a.L * ((heads + a.G) * (a.D - a.pairs) + (int64_t)a.G * a.D), 256);
   } else {
     p.tiles = (int)(ceil_div(a.L, kAppendTile) + 1);
-    p.turners = (int)ceil_div(heads + a.G, kAppendHeads), p.sharers = (int)ceil_div(a.G, kAppendHeads);
-    p.groups = (int64_t)a.B * p.tiles * (p.turners + p.sharers);
+    for (p.chunk = 8; p.chunk >= 1; p.chunk /= 2) {
+      p.turners = (int)ceil_div(heads + a.G, p.chunk), p.sharers = (int)ceil_div(a.G, p.chunk);
+      p.groups = (int64_t)a.B * p.tiles * (p.turners + p.sharers);
+      if (p.chunk == 1 || p.groups >= 3 * cus) break;
+    }
   }
   return p;
 }
@@ -103,7 +109,7 @@ inline bool append_fits(const sc_cache_append& a) {
   const int64_t heads = (a.q ? a.H : 0) + 2LL * a.G;
   if (a.L < 16) return (int64_t)a.B * a.L < (1LL << 32) && (int64_t)a.B * a.L * heads * a.D < (kMostGroups << 8);
   const int64_t tiles = a.B * (ceil_div(a.L, kAppendTile) + 1);
-  return tiles < kMostGroups && tiles * (ceil_div(heads, kAppendHeads) + 1) < kMostGroups;
+  return tiles < kMostGroups && tiles * (ceil_div(heads, 8) + 1) < kMostGroups;  // (smaller chunks make few workgroups)
 }
 
 constexpr int kCopyBytes = 16384;  // of a page, by one workgroup

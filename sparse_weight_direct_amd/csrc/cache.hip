@@ -14,7 +14,8 @@ namespace {
 // ---- Append
 //
 // A pair turns by theta = freq * position.  theta / 2 pi is made and reduced to one turn in fp64 (positions of
-// 10^6 keep 2^-33 of a turn), its sine and cosine in fp32.
+// 10^6 keep 2^-33 of a turn); its sine and cosine are the hardware's, which take turns and are off by 2^-22.9 at
+// most over a whole turn (4 million places; the math library's sincospi is five times the instructions).
 
 constexpr int kTile = kAppendTile;
 
@@ -41,7 +42,9 @@ __device__ __forceinline__ int page_at(const sc_cache_append& a, int b, int t) {
 
 __device__ __forceinline__ void turn(double freq, int position, float& c, float& s) {
   const double turns = (double)position * (freq * 0.15915494309189535);
-  sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
+  const float part = (float)(turns - rint(turns));
+  s = __builtin_amdgcn_sinf(part);
+  c = __builtin_amdgcn_cosf(part);
 }
 
 // Dims of pair j.
@@ -108,16 +111,18 @@ __global__ __launch_bounds__(256) void append_few(const sc_cache_append a, int64
 
 // 8 values of a row from position i on; those outside 0 .. len-1 are 0.
 template <class T>
-__device__ __forceinline__ void load8(const T* p, int i, int len, float (&v)[8]) {
+__device__ __forceinline__ typename Pack<T, 8>::type load8(const T* p, int i, int len) {
   typedef typename Pack<T, 8>::type V;
-  if (i >= 0 && i + 8 <= len) {
-    const V w = *reinterpret_cast<const V*>(p + i);
+  if (i >= 0 && i + 8 <= len) return *reinterpret_cast<const V*>(p + i);
+  V v;
 #pragma unroll
-    for (int j = 0; j < 8; j++) v[j] = (float)w[j];
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; j++) v[j] = i + j >= 0 && i + j < len ? (float)p[i + j] : 0.0f;
+  for (int j = 0; j < 8; j++) {
+    const int at = i + j;
+    T x = T(0);
+    if (at >= 0 && at < len) x = p[at];
+    v[j] = x;
   }
+  return v;
 }
 
 // To positions i .. i+7 of a row of `len`.
@@ -168,8 +173,10 @@ __global__ __launch_bounds__(256) void append_prompt(const sc_cache_append a, in
       const T* x = static_cast<const T*>(a.v) + b * a.v_batch + (int64_t)g * a.D * a.v_channel;
       K* to = static_cast<K*>(a.v_pages) + page * a.v_page + (int64_t)g * a.D * a.P + in;
       for (int d = row; d < a.D; d += 32) {
+        const auto r = load8(x + d * a.v_channel, i, s.len);
         float v[8];
-        load8(x + d * a.v_channel, i, s.len, v);
+#pragma unroll
+        for (int k = 0; k < 8; k++) v[k] = (float)r[k];
         store8(to + d * a.P - i, i, s.len, v);
       }
     }
@@ -181,15 +188,19 @@ __global__ __launch_bounds__(256) void append_prompt(const sc_cache_append a, in
     const int j = row + 32 * p, axis = j < a.pairs ? axis_of(a, j) : -1;
     const double freq = axis >= 0 ? a.freqs[j] : 0.0;
     const int32_t* where = a.positions && axis >= 0 ? a.positions + b * a.positions_batch + axis * a.positions_axis : nullptr;
+    typename Pack<int32_t, 8>::type at;
+    if (where) at = load8(where, i, s.len);
 #pragma unroll
     for (int k = 0; k < 8; k++) {
-      const int n = i + k;
       c[p][k] = 1.0f, sn[p][k] = 0.0f;
-      if (axis >= 0 && n >= 0 && n < s.len) turn(freq, where ? where[n] : t0 + at8 + k, c[p][k], sn[p][k]);
+      if (axis >= 0) turn(freq, where ? at[k] : t0 + at8 + k, c[p][k], sn[p][k]);
     }
   }
-  const int h1 = min((part + 1) * chunk, heads + a.G);
-  for (int h = part * chunk; h < h1; h++) {
+  typedef typename Pack<T, 8>::type V8;
+  int pages[kTile / 16];  // of the tile's sixteens
+#pragma unroll
+  for (int n = 0; n < kTile / 16; n++) pages[n] = page_at(a, b, t0 + 16 * n);
+  for (int h = part; h < heads + a.G; h += turners) {  // some of q's and some of k's
     const bool query = h < heads;
     const T* x = query ? static_cast<const T*>(a.q) + b * a.q_batch + (int64_t)h * a.D * a.q_channel
                        : static_cast<const T*>(a.k) + b * a.k_batch + (int64_t)(h - heads) * a.D * a.k_channel;
@@ -209,22 +220,22 @@ __global__ __launch_bounds__(256) void append_prompt(const sc_cache_append a, in
       const int j = row + 32 * p;
       if (j >= a.pairs) continue;
       const int d0 = first_of(a, j), d1 = second_of(a, j), axis = axis_of(a, j);
+      const V8 r0 = load8(x + d0 * xs, i, s.len), r1 = load8(x + d1 * xs, i, s.len);
       float v0[8], v1[8];
-      load8(x + d0 * xs, i, s.len, v0);
-      load8(x + d1 * xs, i, s.len, v1);
-      if (axis >= 0)
 #pragma unroll
-        for (int k = 0; k < 8; k++) {
-          const float w = v0[k];
-          v0[k] = w * c[p][k] - v1[k] * sn[p][k];
-          v1[k] = v1[k] * c[p][k] + w * sn[p][k];
-        }
+      for (int k = 0; k < 8; k++) {
+        const float u = (float)r0[k], w = (float)r1[k];
+        v0[k] = axis >= 0 ? u * c[p][k] - w * sn[p][k] : u;
+        v1[k] = axis >= 0 ? w * c[p][k] + u * sn[p][k] : w;
+      }
       put(d0, v0);
       put(d1, v1);
     }
     for (int d = 2 * a.pairs + row; d < a.D; d += 32) {
+      const V8 r = load8(x + d * xs, i, s.len);
       float v[8];
-      load8(x + d * xs, i, s.len, v);
+#pragma unroll
+      for (int k = 0; k < 8; k++) v[k] = (float)r[k];
       put(d, v);
     }
     if (!query) {
@@ -234,7 +245,7 @@ __global__ __launch_bounds__(256) void append_prompt(const sc_cache_append a, in
       for (int e = tid; e < kTile * pieces; e += 256) {
         const int n = e / pieces, d = e % pieces * 8, t = t0 + n;
         if (t < s.past || t >= s.past + s.len) continue;
-        const int pg = page_at(a, b, t);
+        const int pg = n < 32 ? n < 16 ? pages[0] : pages[1] : n < 48 ? pages[2] : pages[3];
         if (pg < 0) continue;
         *reinterpret_cast<V*>(static_cast<K*>(a.k_pages) + pg * a.k_page + ((int64_t)(h - heads) * a.P + t % a.P) * a.D + d) =
             *reinterpret_cast<const V*>(keys + n * pitch + d);
@@ -244,16 +255,16 @@ __global__ __launch_bounds__(256) void append_prompt(const sc_cache_append a, in
 }
 
 template <class T, class K>
-int launch_append(const sc_cache_append& a, hipStream_t st) {
+int launch_append(const sc_cache_append& a, int cus, hipStream_t st) {
   const int heads = a.q ? a.H : 0;
-  const AppendPlan p = append_plan(a);
+  const AppendPlan p = append_plan(a, cus);
   const dim3 grid((unsigned)p.groups);
   if (p.few) {
     const int64_t total = (int64_t)a.B * a.L * ((int64_t)(heads + a.G) * (a.D - a.pairs) + (int64_t)a.G * a.D);
     hipLaunchKernelGGL((append_few<T, K>), dim3((unsigned)ceil_div(total, 256)), dim3(256), 0, st, a, total);
     return (int)hipGetLastError();
   }
-  const int tiles = p.tiles, chunk = kAppendHeads, turners = p.turners, sharers = p.sharers;
+  const int tiles = p.tiles, chunk = p.chunk, turners = p.turners, sharers = p.sharers;
   const int lds = kTile * key_pitch<K>(a.D) * (int)sizeof(K);
   if (a.pairs <= 32)
     hipLaunchKernelGGL((append_prompt<T, K, 1>), grid, dim3(256), lds, st, a, tiles, turners, sharers, chunk);
@@ -293,13 +304,13 @@ __global__ __launch_bounds__(256) void copy_pages(const sc_cache_copy a, int pie
 
 }  // namespace
 
-int launch_cache_append(const sc_cache_append& a, void* stream) {
+int launch_cache_append(const sc_cache_append& a, int cus, void* stream) {
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  if (a.dtype == SC_BF16) return launch_append<__bf16, __bf16>(a, st);
-  if (a.dtype == SC_F16) return launch_append<_Float16, _Float16>(a, st);
-  if (a.cache_dtype == SC_BF16) return launch_append<float, __bf16>(a, st);
-  if (a.cache_dtype == SC_F16) return launch_append<float, _Float16>(a, st);
-  return launch_append<float, float>(a, st);
+  if (a.dtype == SC_BF16) return launch_append<__bf16, __bf16>(a, cus, st);
+  if (a.dtype == SC_F16) return launch_append<_Float16, _Float16>(a, cus, st);
+  if (a.cache_dtype == SC_BF16) return launch_append<float, __bf16>(a, cus, st);
+  if (a.cache_dtype == SC_F16) return launch_append<float, _Float16>(a, cus, st);
+  return launch_append<float, float>(a, cus, st);
 }
 
 int launch_cache_copy(const sc_cache_copy& a, void* stream) {
