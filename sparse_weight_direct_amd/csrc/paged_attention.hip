@@ -169,24 +169,26 @@ struct Rows {
     return any;
   }
 
-  // Whether every row sees all of keys k0 .. k0+31 (`miss`: halves of them that are on no page).
-  __device__ __forceinline__ bool whole(int k0, int miss) const {
+  // Whether every row sees all of `size` keys from k0 on (`miss`: halves of them that are on no page).
+  __device__ __forceinline__ bool whole(int k0, int miss, int size = kBlock) const {
     const int first = r.past + r.first, last = r.past + r.last;
-    return !miss && k0 + kBlock <= r.end &&
-           (k0 + kBlock <= r.prefix || (k0 + kBlock - 1 <= first && (!a.window || k0 >= last - a.window + 1)));
+    return !miss && k0 + size <= r.end &&
+           (k0 + size <= r.prefix || (k0 + size - 1 <= first && (!a.window || k0 >= last - a.window + 1)));
   }
   __device__ __forceinline__ bool hidden(int lanes, int k0, int miss, int u, int t, int i) const {
     const int key = k0 + key_of(lanes, u, i);
     return (((miss >> (kWide ? u : lanes >> 1)) & 1) != 0) | ((key >= pre[t]) & ((key > most_key[t]) | (key < low[t])));
   }
 
-  // From the products q . k to the weights, in s and (rounded) in p; sums and totals follow the maximum.
-  __device__ __forceinline__ void weigh(F4 (&s)[2][NT], V (&p)[NT][VF], int k0, int miss, bool all) {
+  // From the products q . k of NB blocks of keys from k0 on to the weights, rounded; sums and totals follow the maximum.
+  // (`miss`: two bits a block.)
+  template <int NB>
+  __device__ __forceinline__ void weigh(F4 (&s)[2 * NB][NT], V (&p)[NT][NB * VF], int k0, int miss, bool all) {
     float scale = a.scale * kLog2e;
     if (a.cap > 0.0f || a.slopes || !(scale > 0.0f)) {  // else the maximum is looked for among the products themselves
       const float by = a.cap > 0.0f ? a.scale / a.cap : scale, cap = a.cap * kLog2e;
 #pragma unroll
-      for (int u = 0; u < 2; u++)
+      for (int u = 0; u < 2 * NB; u++)
 #pragma unroll
         for (int t = 0; t < NT; t++) {
           F4 v = s[u][t];
@@ -194,7 +196,7 @@ struct Rows {
           for (int i = 0; i < 4; i++) {
             v[i] *= by;
             if (a.cap > 0.0f) v[i] = cap * tanh_of<T>(v[i]);
-            if (a.slopes) v[i] -= slope[t] * fabsf((float)(pos[t] - k0 - key_of(part, u, i)));
+            if (a.slopes) v[i] -= slope[t] * fabsf((float)(pos[t] - k0 - (u / 2) * kBlock - key_of(part, u & 1, i)));
           }
           s[u][t] = v;
         }
@@ -203,12 +205,12 @@ struct Rows {
     // without branches: elements of a vector that were written under a lane's condition came out wrong here
     if (!all)
 #pragma unroll
-      for (int u = 0; u < 2; u++)
+      for (int u = 0; u < 2 * NB; u++)
 #pragma unroll
         for (int t = 0; t < NT; t++) {
           F4 v = s[u][t];
 #pragma unroll
-          for (int i = 0; i < 4; i++) v[i] = hidden(part, k0, miss, u, t, i) ? -kInf : v[i];
+          for (int i = 0; i < 4; i++) v[i] = hidden(part, k0 + (u / 2) * kBlock, miss >> (u & ~1), u & 1, t, i) ? -kInf : v[i];
           s[u][t] = v;
         }
     // the maximum moves where a score passes it by 2^8 (the first ones do)
@@ -216,8 +218,10 @@ struct Rows {
     float most[NT];
 #pragma unroll
     for (int t = 0; t < NT; t++) {
-      most[t] = fmaxf(fmaxf(fmaxf(s[0][t][0], s[0][t][1]), fmaxf(s[0][t][2], s[0][t][3])),
-                      fmaxf(fmaxf(s[1][t][0], s[1][t][1]), fmaxf(s[1][t][2], s[1][t][3]))) * scale;
+      most[t] = -kInf;
+#pragma unroll
+      for (int u = 0; u < 2 * NB; u++) most[t] = fmaxf(most[t], fmaxf(fmaxf(s[u][t][0], s[u][t][1]), fmaxf(s[u][t][2], s[u][t][3])));
+      most[t] *= scale;
       moves |= most[t] > top[t] + 8.0f;
     }
     if (__any(moves))
@@ -233,14 +237,14 @@ struct Rows {
 #pragma unroll
     for (int t = 0; t < NT; t++)
 #pragma unroll
-      for (int u = 0; u < 2; u++) {
+      for (int u = 0; u < 2 * NB; u++) {
         F4 w = s[u][t];
 #pragma unroll
         for (int i = 0; i < 4; i++) w[i] = exp2_fast(fmaf(w[i], scale, -use[t]));
         s[u][t] = w;
         if (kWide) total[t][0] += (w[0] + w[1]) + (w[2] + w[3]);
 #pragma unroll
-        for (int i = 0; i < 4; i++) p[t][kWide ? u : 0][kWide ? i : 4 * u + i] = T(w[i]);
+        for (int i = 0; i < 4; i++) p[t][kWide ? u : u / 2][kWide ? i : 4 * (u & 1) + i] = T(w[i]);
       }
     // the rounded weights are summed as they are used: a sum over rows of ones on the matrix cores
     if constexpr (!kWide) {
@@ -248,7 +252,9 @@ struct Rows {
 #pragma unroll
       for (int j = 0; j < N; j++) ones[j] = T(1.0f);
 #pragma unroll
-      for (int t = 0; t < NT; t++) total[t] = mma(ones, p[t][0], total[t]);
+      for (int t = 0; t < NT; t++)
+#pragma unroll
+        for (int n = 0; n < NB; n++) total[t] = mma(ones, p[t][n], total[t]);
     }
   }
 
@@ -259,8 +265,9 @@ struct Rows {
   // and zeros say which rows see a +infinity or NaN, and which a -infinity or NaN.  value(d, f): a lane's values.
   // It takes so many registers that the walk over the context knows nothing of it: where a sum is not finite at
   // its end (which is seldom), the walk is made again with it.
-  template <class Value>
-  __device__ __forceinline__ void add_odd(const V (&p)[NT][VF], int k0, int miss, Value value) {
+  // (p's from f0 on are the block's)
+  template <int NF, class Value>
+  __device__ __forceinline__ void add_odd(const V (&p)[NT][NF], int f0, int k0, int miss, Value value) {
     int lanes = part;
     asm volatile("" : "+v"(lanes));  // keeps what is made of it out of the loop's registers
     V seen[NT][VF];
@@ -291,7 +298,7 @@ struct Rows {
           F4 odd;
 #pragma unroll
           for (int i = 0; i < 4; i++) odd[i] = (ups[i] > 0.0f ? kInf : 0.0f) - (downs[i] > 0.0f ? kInf : 0.0f);
-          o[d][t] = mma(rest, p[t][f], o[d][t]) + odd;
+          o[d][t] = mma(rest, p[t][f0 + f], o[d][t]) + odd;
         }
       }
   }
@@ -429,7 +436,7 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : NT
       if (!kAhead) load_v(at);
       const bool whole = rows.whole(k0, miss);
       V p[NT][VF];
-      rows.weigh(s, p, k0, miss, whole);
+      rows.template weigh<1>(s, p, k0, miss, whole);
       if (!whole) {  // nothing that is not there reaches the product
 #pragma unroll
         for (int f = 0; f < VF; f++) {
@@ -442,7 +449,7 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : NT
         }
       }
       if (odd && !whole) {
-        rows.add_odd(p, k0, miss, [&](int d, int f) { return vf[d][f]; });
+        rows.add_odd(p, 0, k0, miss, [&](int d, int f) { return vf[d][f]; });
       } else {
 #pragma unroll
         for (int f = 0; f < VF; f++)
@@ -563,6 +570,7 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
   typedef Stage<T, DT> S;
   typedef typename R::V V;
   constexpr int N = R::N, KF = R::KF, VF = R::VF, DM = R::DM, KT = S::KT;
+  constexpr int NB = KT / kBlock, kEarly = 4;
   constexpr int KI = S::kKeys / 4096;                      // copies of a wavefront's for the keys, and as many for the values
   constexpr int RK = 64 / S::CK, RV = 64 / S::CV;          // rows of one copy
   __shared__ __align__(256) char lds[2 * S::kBytes];
@@ -593,13 +601,29 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
   const T* v_head = static_cast<const T*>(a.v_pages) + (int64_t)g * a.P * a.D;
   // copies a tile; returns which sixteens of its keys are on no page
   auto copy = [&](int k0, int buffer) __attribute__((always_inline)) {
+    const uint32_t to = base + buffer * S::kBytes + wave * 1024;
+    if (a.P >= KT) {  // one page holds the tile
+      const int at = page_of(a, table, k0 >> shift), page = max(at, 0), in = k0 & (a.P - 1);
+      const T* keys = k_head + page * a.k_page + in * a.D;
+      const T* values = v_head + page * a.v_page + in;
+#pragma unroll
+      for (int i = 0; i < KI; i++) {
+        const int key = RK * (4 * i + wave) + kr, c = S::key_piece(key, kc) * N;
+        if (EXACT || c < a.D) to_lds(to + i * 4096, keys, (key * a.D + c) * (int)sizeof(T));
+      }
+#pragma unroll
+      for (int i = 0; i < KI; i++) {
+        const int d = RV * (4 * i + wave) + vr;
+        if (EXACT || d < a.D) to_lds(to + S::kKeys + i * 4096, values, (d * a.P + vc) * (int)sizeof(T));
+      }
+      return at < 0 ? (1 << KT / 16) - 1 : 0;
+    }
     int page[KT / 16], miss = 0;
 #pragma unroll
     for (int h = 0; h < KT / 16; h++) {
       page[h] = page_of(a, table, (k0 + 16 * h) >> shift);
       if (page[h] < 0) page[h] = 0, miss |= 1 << h;
     }
-    const uint32_t to = base + buffer * S::kBytes + wave * 1024;
 #pragma unroll
     for (int i = 0; i < KI; i++) {
       const int first = RK * (4 * i + wave), c = S::key_piece(first + kr, kc) * N;
@@ -609,23 +633,14 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
       const T* from = k_head + pg * a.k_page + ((k0 + first) & (a.P - 1)) * a.D;  // its RK keys are one page's
       if (EXACT || c < a.D) to_lds(to + i * 4096, from, (kr * a.D + c) * (int)sizeof(T));
     }
-    if (a.P >= KT) {
-      const T* from = v_head + page[0] * a.v_page + (k0 & (a.P - 1));
+    int pg = page[0];
 #pragma unroll
-      for (int i = 0; i < KI; i++) {
-        const int first = RV * (4 * i + wave);
-        if (EXACT || first + vr < a.D) to_lds(to + S::kKeys + i * 4096, from + first * a.P, (vr * a.P + vc) * (int)sizeof(T));
-      }
-    } else {
-      int pg = page[0];
+    for (int h = 1; h < KT / 16; h++) pg = vc >> 4 == h ? page[h] : pg;
+    const T* from = v_head + pg * a.v_page + ((k0 + vc) & (a.P - 1)) + vr * a.P;
 #pragma unroll
-      for (int h = 1; h < KT / 16; h++) pg = vc >> 4 == h ? page[h] : pg;
-      const T* from = v_head + pg * a.v_page + ((k0 + vc) & (a.P - 1)) + vr * a.P;
-#pragma unroll
-      for (int i = 0; i < KI; i++) {
-        const int first = RV * (4 * i + wave);
-        if (EXACT || first + vr < a.D) to_lds(to + S::kKeys + i * 4096, from + first * a.P);
-      }
+    for (int i = 0; i < KI; i++) {
+      const int first = RV * (4 * i + wave);
+      if (EXACT || first + vr < a.D) to_lds(to + S::kKeys + i * 4096, from + first * a.P);
     }
     return miss;
   };
@@ -660,42 +675,44 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
         }
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
       }
+      if (here >= until || (here + KT <= from && here >= r.prefix)) continue;
+      F4 s[2 * NB][NT];
 #pragma unroll
-      for (int kb = 0; kb < KT / kBlock; kb++) {
-        const int at = here + kb * kBlock, lost = gone >> (2 * kb) & 3;
-        if (at >= until || (at + kBlock <= from && at >= r.prefix)) continue;
-        F4 s[2][NT];
+      for (int u = 0; u < 2 * NB; u++) {
+        const int key = (u / 2) * kBlock + R::key_row(u & 1, col);
+        V kf[KF];
 #pragma unroll
-        for (int u = 0; u < 2; u++) {
-          const int key = kb * kBlock + R::key_row(u, col);
-          V kf[KF];
+        for (int f = 0; f < KF; f++) kf[f] = *reinterpret_cast<const V*>(keys + key * S::kKeyRow + S::key_piece(key, 4 * f + part) * 16);
 #pragma unroll
-          for (int f = 0; f < KF; f++) kf[f] = *reinterpret_cast<const V*>(keys + key * S::kKeyRow + S::key_piece(key, 4 * f + part) * 16);
+        for (int t = 0; t < NT; t++) {
+          s[u][t] = F4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int t = 0; t < NT; t++) {
-            s[u][t] = F4{0.0f, 0.0f, 0.0f, 0.0f};
+          for (int f = 0; f < KF; f++) s[u][t] = mma(kf[f], rows.q[t][f], s[u][t]);
+        }
+      }
+      auto value = [&](int d, int f) __attribute__((always_inline)) {
+        return *reinterpret_cast<const V*>(values + (d * 16 + col) * S::kValueRow + S::value_piece(d * 16 + col, f * 4 + part) * 16);
+      };
+      // the first values are on their way while the weights are made
+      V early[kEarly];
 #pragma unroll
-            for (int f = 0; f < KF; f++) s[u][t] = mma(kf[f], rows.q[t][f], s[u][t]);
+      for (int d = 0; d < kEarly; d++) early[d] = value(d, 0);
+      const bool whole = rows.whole(here, gone, KT);
+      V p[NT][NB * VF];
+      rows.template weigh<NB>(s, p, here, gone, whole);
+      if (odd && !whole) {
+#pragma unroll
+        for (int kb = 0; kb < NB; kb++)
+          rows.add_odd(p, kb * VF, here + kb * kBlock, gone >> (2 * kb), [&](int d, int f) { return value(d, kb * VF + f); });
+      } else {
+#pragma unroll
+        for (int f = 0; f < NB * VF; f++)
+#pragma unroll
+          for (int d = 0; d < DM; d++) {
+            const V v = f == 0 && d < kEarly ? early[d & (kEarly - 1)] : value(d, f);
+#pragma unroll
+            for (int t = 0; t < NT; t++) rows.o[d][t] = mma(v, p[t][f], rows.o[d][t]);
           }
-        }
-        const bool whole = rows.whole(at, lost);
-        V p[NT][VF];
-        rows.weigh(s, p, at, lost, whole);
-        auto value = [&](int d, int f) {
-          return *reinterpret_cast<const V*>(values + (d * 16 + col) * S::kValueRow + S::value_piece(d * 16 + col, (kb * VF + f) * 4 + part) * 16);
-        };
-        if (odd && !whole) {
-          rows.add_odd(p, at, lost, value);
-        } else {
-#pragma unroll
-          for (int f = 0; f < VF; f++)
-#pragma unroll
-            for (int d = 0; d < DM; d++) {
-              const V v = value(d, f);
-#pragma unroll
-              for (int t = 0; t < NT; t++) rows.o[d][t] = mma(v, p[t][f], rows.o[d][t]);
-            }
-        }
       }
     }
   };
