@@ -24,7 +24,7 @@ struct AttendPlan {
 };
 
 // Tiles of rows whose queries and sums leave a wavefront's registers room for a block's keys and values.
-constexpr int attend_most_tiles(int64_t size, int dims) { return size * dims <= 256 ? 4 : size * dims <= 512 ? 2 : 1; }
+constexpr int attend_most_tiles(int64_t size, int dims) { return dims <= 64 ? 4 : size * dims <= 512 ? 2 : 1; }
 constexpr int attend_staged_tiles(int64_t size, int dims) { return size * dims <= 512 ? 2 : 1; }
 
 // How the context is cut.  Single positions, 8 heads of keys of 128 dims with 4 of queries each, bf16, us:
@@ -42,11 +42,23 @@ constexpr int attend_staged_tiles(int64_t size, int dims) { return size * dims <
 //
 // so enough pieces for two workgroups a CU, of eight blocks of 32 keys at least, at most 32; and where there are enough without
 // cutting, four of 64 blocks at least: sequences' lengths differ as a rule, and evenly long ones lose less than that gains.
+//
+// From how many rows on the wavefronts share the keys, us, shared / each its own (16 heads over 4, contexts 1 x 30000,
+// 8 x 4000, 64 x 500):
+//
+//   rows        32                            48                             64                             96
+//   bf16, 64    30/21    26/18    25/17       31/25    25/24    25/23        31/27    25/25    27/24        31/27    26/27    28/22
+//   bf16, 128   41/30    35/27    38/26       41/49    35/62    39/62        41/50    37/66    41/67        42/54    38/74    43/71
+//   bf16, 256   130/99   118/102  121/99      130/112  118/138  124/125      132/113  121/140  130/143      135/185  124/214  134/202
+//   fp32, 64    82/33    59/30    53/26       82/53    59/54    54/46        82/54    60/55    60/51        83/56    61/65    60/68
+//   fp32, 128   155/58   110/62   106/54      155/62   111/75   109/64       156/63   112/76   113/75       157/107  115/128  117/109
+//
+// so above 32 rows for 16-bit types of more than 64 dims, else from 96 on.
 inline AttendPlan attend_plan(const sc_paged_attention& a, int cus) {
   AttendPlan p;
   const int64_t share = a.H / a.G, rows = share * a.L, size = a.dtype == SC_F32 ? 4 : 2;
   const int dims = a.D <= 64 ? 64 : a.D <= 128 ? 128 : 256;
-  p.staged = rows >= 128;
+  p.staged = size == 2 && dims > 64 ? rows > 32 : rows >= 96;
   p.nt = p.staged ? attend_staged_tiles(size, dims) : std::min(attend_most_tiles(size, dims), rows <= 16 ? 1 : rows <= 32 ? 2 : 4);
   const int tile = p.rows();
   p.pitch = a.L < tile ? a.L : (int)(ceil_div(a.L, tile) * tile);
