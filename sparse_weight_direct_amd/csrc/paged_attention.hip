@@ -358,12 +358,13 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : NT
   __shared__ float lds[4 * 16 * kPitch];
   __shared__ float2 tops[4][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, part = lane >> 4;
-  // the pieces one after another: those that have no blocks would else leave whole groups of CUs idle
-  const int each = gridDim.x / cut.splits, split = blockIdx.x / each;
-  int id = xcd_logical(blockIdx.x % each, each);
-  const int tile = id % cut.tiles;
-  id /= cut.tiles;
-  const int g = id % a.G, b = id / a.G, share = a.H / a.G, row0 = tile * 16 * NT;
+  // the heads of keys side by side, so that every XCD (workgroups go round them) has its part of each sequence, however
+  // long; the pieces one after another: those that have no blocks would else leave whole groups of CUs idle
+  int id = blockIdx.x;
+  const int heads = a.B * a.G, bg = id % heads;
+  id /= heads;
+  const int tile = id % cut.tiles, split = id / cut.tiles;
+  const int g = bg % a.G, b = bg / a.G, share = a.H / a.G, row0 = tile * 16 * NT;
   const Reach r = reach_of(a, b, row0, 16 * NT, cut.pitch);
   const Blocks blocks(a, r, kBlock);
   const int per = (blocks.count + cut.splits - 1) / cut.splits, stop = min(blocks.count, (split + 1) * per);
@@ -493,7 +494,7 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : NT
 #pragma unroll
     for (int w = 0; w < 4; w++) none = none & (tops[w][row].y == 0.0f);
     none = none | (i >= r.len);  // (where whole blocks are seen, rows that are not there saw them too)
-    const int64_t ws_row = ((int64_t)(b * a.G + g) * cut.tiles + tile) * (16 * NT) + t * 16 + row;
+    const int64_t ws_row = ((int64_t)bg * cut.tiles + tile) * (16 * NT) + t * 16 + row;
     const float by = none ? 0.0f : cut.splits > 1 ? 1.0f : seen ? 1.0f / l : __builtin_nanf("");
     const int64_t ws = ws_row * cut.splits + split;
     if (cut.splits > 1 && piece == 0) cut.tops[ws] = make_float2(none ? -kInf : m, none ? 0.0f : seen ? l : __builtin_nanf(""));
