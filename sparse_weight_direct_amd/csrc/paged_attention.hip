@@ -181,9 +181,9 @@ struct Rows {
   }
 
   // From the products q . k of NB blocks of keys from k0 on to the weights, rounded; sums and totals follow the maximum.
-  // (`miss`: two bits a block.)
-  template <int NB>
-  __device__ __forceinline__ void weigh(F4 (&s)[2 * NB][NT], V (&p)[NT][NB * VF], int k0, int miss, bool all) {
+  // (`miss`: two bits a block.)  With FINE, 16-bit types get what the rounding lost as a second operand.
+  template <int NB, bool FINE>
+  __device__ __forceinline__ void weigh(F4 (&s)[2 * NB][NT], V (&p)[NT][NB * VF], V (&rest)[NT][FINE ? NB * VF : 1], int k0, int miss, bool all) {
     float scale = a.scale * kLog2e;
     if (a.cap > 0.0f || a.slopes || !(scale > 0.0f)) {  // else the maximum is looked for among the products themselves
       const float by = a.cap > 0.0f ? a.scale / a.cap : scale, cap = a.cap * kLog2e;
@@ -245,6 +245,9 @@ struct Rows {
         if (kWide) total[t][0] += (w[0] + w[1]) + (w[2] + w[3]);
 #pragma unroll
         for (int i = 0; i < 4; i++) p[t][kWide ? u : u / 2][kWide ? i : 4 * (u & 1) + i] = T(w[i]);
+        if constexpr (FINE && !kWide)
+#pragma unroll
+          for (int i = 0; i < 4; i++) rest[t][u / 2][4 * (u & 1) + i] = T(w[i] - (float)T(w[i]));
       }
     // the rounded weights are summed as they are used: a sum over rows of ones on the matrix cores
     if constexpr (!kWide) {
@@ -254,7 +257,10 @@ struct Rows {
 #pragma unroll
       for (int t = 0; t < NT; t++)
 #pragma unroll
-        for (int n = 0; n < NB; n++) total[t] = mma(ones, p[t][n], total[t]);
+        for (int n = 0; n < NB; n++) {
+          total[t] = mma(ones, p[t][n], total[t]);
+          if constexpr (FINE) total[t] = mma(ones, rest[t][n], total[t]);
+        }
     }
   }
 
@@ -266,8 +272,8 @@ struct Rows {
   // It takes so many registers that the walk over the context knows nothing of it: where a sum is not finite at
   // its end (which is seldom), the walk is made again with it.
   // (p's from f0 on are the block's)
-  template <int NF, class Value>
-  __device__ __forceinline__ void add_odd(const V (&p)[NT][NF], int f0, int k0, int miss, Value value) {
+  template <bool FINE, int NF, int NR, class Value>
+  __device__ __forceinline__ void add_odd(const V (&p)[NT][NF], const V (&rest)[NT][NR], int f0, int k0, int miss, Value value) {
     int lanes = part;
     asm volatile("" : "+v"(lanes));  // keeps what is made of it out of the loop's registers
     V seen[NT][VF];
@@ -291,14 +297,15 @@ struct Rows {
           x[j] = odd & (nan | ~neg) & Bits<T>::kOnes;
           y[j] = odd & (nan | neg) & Bits<T>::kOnes;
         }
-        const V rest = __builtin_bit_cast(V, w), up = __builtin_bit_cast(V, x), down = __builtin_bit_cast(V, y);
+        const V finite = __builtin_bit_cast(V, w), up = __builtin_bit_cast(V, x), down = __builtin_bit_cast(V, y);
 #pragma unroll
         for (int t = 0; t < NT; t++) {
           const F4 none = {0.0f, 0.0f, 0.0f, 0.0f}, ups = mma(up, seen[t][f], none), downs = mma(down, seen[t][f], none);
           F4 odd;
 #pragma unroll
           for (int i = 0; i < 4; i++) odd[i] = (ups[i] > 0.0f ? kInf : 0.0f) - (downs[i] > 0.0f ? kInf : 0.0f);
-          o[d][t] = mma(rest, p[t][f0 + f], o[d][t]) + odd;
+          o[d][t] = mma(finite, p[t][f0 + f], o[d][t]) + odd;
+          if constexpr (FINE) o[d][t] = mma(finite, rest[t][f0 + f], o[d][t]);
         }
       }
   }
@@ -347,7 +354,8 @@ __device__ __forceinline__ int page_of(const sc_paged_attention& a, const int32_
 //
 // A workgroup has 16 NT rows of one head of keys and a piece of the context; its four wavefronts take its
 // blocks in turn, operands straight from the cache to registers (each byte is read once), the next block's on their
-// way while one is computed, and their sums are joined at the end.
+// way while one is computed, and their sums are joined at the end.  Bound by the cache's bytes, so the matrix cores have time for
+// weights of twice 16 bits: a weight and what its rounding lost are two operands, and an output is as exact as its own rounding.
 template <class T, int DT, int NT>
 __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : NT > 1 || (DT == 128 && sizeof(T) == 2) ? 2 : 3) void attend_direct(const sc_paged_attention a, const Cut cut) {
   typedef Rows<T, DT, NT> R;
@@ -436,8 +444,8 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : NT
       if (kAhead && more) load_k(next);
       if (!kAhead) load_v(at);
       const bool whole = rows.whole(k0, miss);
-      V p[NT][VF];
-      rows.template weigh<1>(s, p, k0, miss, whole);
+      V p[NT][VF], rest[NT][R::kWide ? 1 : VF];
+      rows.template weigh<1, !R::kWide>(s, p, rest, k0, miss, whole);
       if (!whole) {  // nothing that is not there reaches the product
 #pragma unroll
         for (int f = 0; f < VF; f++) {
@@ -450,14 +458,17 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : NT
         }
       }
       if (odd && !whole) {
-        rows.add_odd(p, 0, k0, miss, [&](int d, int f) { return vf[d][f]; });
+        rows.template add_odd<!R::kWide>(p, rest, 0, k0, miss, [&](int d, int f) { return vf[d][f]; });
       } else {
 #pragma unroll
         for (int f = 0; f < VF; f++)
 #pragma unroll
           for (int d = 0; d < DM; d++)
 #pragma unroll
-            for (int t = 0; t < NT; t++) rows.o[d][t] = mma(vf[d][f], p[t][f], rows.o[d][t]);
+            for (int t = 0; t < NT; t++) {
+              rows.o[d][t] = mma(vf[d][f], p[t][f], rows.o[d][t]);
+              if constexpr (!R::kWide) rows.o[d][t] = mma(vf[d][f], rest[t][f], rows.o[d][t]);
+            }
       }
       if (kAhead && more) load_v(next);
       at = next;
@@ -699,12 +710,12 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
 #pragma unroll
       for (int d = 0; d < kEarly; d++) early[d] = value(d, 0);
       const bool whole = rows.whole(here, gone, KT);
-      V p[NT][NB * VF];
-      rows.template weigh<NB>(s, p, here, gone, whole);
+      V p[NT][NB * VF], none[NT][1];
+      rows.template weigh<NB, false>(s, p, none, here, gone, whole);
       if (odd && !whole) {
 #pragma unroll
         for (int kb = 0; kb < NB; kb++)
-          rows.add_odd(p, kb * VF, here + kb * kBlock, gone >> (2 * kb), [&](int d, int f) { return value(d, kb * VF + f); });
+          rows.template add_odd<false>(p, none, kb * VF, here + kb * kBlock, gone >> (2 * kb), [&](int d, int f) { return value(d, kb * VF + f); });
       } else {
 #pragma unroll
         for (int f = 0; f < NB * VF; f++)
