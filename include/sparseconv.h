@@ -570,9 +570,10 @@ typedef struct {
  * over the visible positions t < past[b] + lengths[b] of head h / (H/G): those with t < prefix[b], and
  * those with t <= past + i and, with a window, past + i - t < window.  (So a prefix is seen whole by
  * every position, also from within it and from beyond the window.)  Where nothing is visible out is 0.
- * What is not visible may hold anything, infinities and NaN included.  Sums and softmax in fp32; the weights
- * p are rounded to dtype for the second product (relative to the row's largest score so far), which is a choice: an output
- * is off by up to half a unit of dtype of its terms' magnitudes beside its own rounding.
+ * What is not visible may hold anything, infinities and NaN included.  Sums and softmax in fp32.  With 16-bit types the weights p
+ * are rounded to dtype for the second product where a head of keys has many rows (H/G * L > 32; up to 64 dims: >= 96), which
+ * is a choice: an output is off by up to half a unit of dtype of its terms' magnitudes beside its own rounding; with
+ * fewer rows they keep twice the bits.  Their sum is that of the rounded weights.
  * B, L >= 0.  Limits: L < 2^30, H, G <= 2^16, and fewer than 2^24 workgroups: B*G*ceil(H/G*L/16) < 2^24
  * with L rounded up to a multiple of 128 from there on.
  */

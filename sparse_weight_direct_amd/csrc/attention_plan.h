@@ -29,19 +29,21 @@ constexpr int attend_staged_tiles(int64_t size, int dims) { return size * dims <
 
 // How the context is cut.  Single positions, 8 heads of keys of 128 dims with 4 of queries each, bf16, us:
 //
-//   pieces                       1      2      4      8      16     32     64
-//   1 sequence of 250           9.6   13.6   13.5
-//   1 of 777                   16.6   15.4   14.1
-//   1 of 8000                                39.0   29.7   18.3   17.9   22.4
-//   1 of 32000                                      78.2   44.6   35.7   39.1
-//   16 of up to 8191            132   80.2   83.8   84.7
-//   64 of 0 to 8191             256    251    241    252
-//   64 of 8191 each             356    366    372    392
-//   fp32, 24 x 16 heads of 64 dims, up to 3000: 95.4, 79.5, 84.4, 88.3; with a window of 1024: 48.6, 44.7, 48.2
-//   512 positions after 30000 (rows shared by wavefronts): 1091, 563, 362, 383
+//   pieces                       1      2      3      4      8      16     32     64
+//   1 sequence of 250           8.9   11.7          11.6
+//   1 of 777                   16.5   15.3          13.3   14.1
+//   1 of 8000                                       39.4   29.7   18.2   17.7   22.0
+//   1 of 32000                                             77.3   44.3   35.2   38.8
+//   16 of 0 to 8191             130   79.5          83.0   78.3
+//   64 of 0 to 8191             267    248   232     227    237
+//   64 of 8191 each             357    366   370     372    390
+//   fp32, 24 x 16 heads of 64 dims, 0 to 3000: 98.2, 81.9, -, 74.9, 75.4; with a window of 1024: 47.3, 43.8, -, 46.4, 53.0
+//   512 positions after 30000 (rows shared by wavefronts): 740, 388, -, 298, 312
+//   333 positions, fp16, 5 x 6 heads of 80 dims (likewise): 74.5, 49.5, -, 39.9, 46.8, with six 37.1
 //
-// so enough pieces for two workgroups a CU, of eight blocks of 32 keys at least, at most 32; and where there are enough without
+// so enough pieces for two workgroups a CU, of six blocks of 32 keys at least, at most 32; and where there are enough without
 // cutting, four of 64 blocks at least: sequences' lengths differ as a rule, and evenly long ones lose less than that gains.
+// Single positions take a power of two of them (1 of 8000 in 31: 20.1).
 //
 // From how many rows on the wavefronts share the keys, us, shared / each its own (16 heads over 4, contexts 1 x 30000,
 // 8 x 4000, 64 x 500):
@@ -64,8 +66,10 @@ inline AttendPlan attend_plan(const sc_paged_attention& a, int cus) {
   p.pitch = a.L < tile ? a.L : (int)(ceil_div(a.L, tile) * tile);
   p.tiles = ceil_div(share * p.pitch, tile);
   const int64_t base = (int64_t)a.B * a.G * p.tiles, blocks = ceil_div((int64_t)a.width * a.P, 32);
-  int64_t pieces = std::min<int64_t>({ceil_div(2 * cus, base), blocks / 8, 32});
+  int64_t pieces = std::min<int64_t>({ceil_div(2 * cus, base), blocks / 6, 32});
   if (!p.staged && base >= 2 * cus && base < 8 * cus) pieces = std::min<int64_t>(4, blocks / 64);
+  if (!p.staged)
+    while (pieces & (pieces - 1)) pieces &= pieces - 1;
   p.splits = (int)std::max<int64_t>(1, pieces);
   return p;
 }
@@ -87,9 +91,9 @@ inline bool attend_fits(const sc_paged_attention& a) {
 // ---- Append
 constexpr int kAppendTile = 64;  // positions of a prompt's tile, whole in the cache: a thread's 8 lie in one page
 
-// Heads of a workgroup: their sines and cosines are made once.  Measured with 1, 2, 4, 8, 12 of them, us, 32 heads of q over 8 of
-// 128 dims, bf16: 2 x 4096 positions 111, 91, 77, 64.5, 66.6; 1 x 512: 12.2, 12.2, 18.5, 30.4, 29.3; 1 x 17: 8.3, 11.1,
-// 17.7, 30.4, 36.4; 16 over 16 of 64 dims, 4 x 1000: 20.8, 18.5, 19.1, 26.1, 31.3.  So as many, up to 8, as leave three workgroups a CU.
+// Heads of a workgroup: their sines and cosines are made once.  Measured with 1, 2, 4, 8 of them, us, 32 heads of q over 8 of
+// 128 dims, bf16: 2 x 4096 positions 63.8, 51.2, 44.8, 44.1; 1 x 512: 9.2, 10.1, 11.1, 16.8; 1 x 17: 7.2, 9.4, 14.2, 23.8;
+// 16 over 16 of 64 dims, 4 x 1000: 20.4, 15.8, 16.8, 21.8.  So as many, up to 8, as leave three workgroups a CU.
 struct AppendPlan {
   int chunk;
   bool few;                        // a thread for every pair of every position

@@ -1,5 +1,6 @@
 // The paged cache's update with rotary positions (sparseconv_cache_append) and copies of its pages
-// (sparseconv_cache_copy).  Both are bound by memory.
+// (sparseconv_cache_copy).  Both are bound by memory: 2 x 4096 positions of 32 + 2 x 8 heads of 128 dims, three coordinates, bf16,
+// 50.6 us in a row of calls, 4.0 TB/s read and written (the kernel alone 43.9; a copy: 5.1); 16 x 200 pages of 64 KB 83 us, 5.1 TB/s.
 #include <hip/hip_runtime.h>
 
 #include "attention.h"
@@ -56,7 +57,9 @@ __device__ __forceinline__ int axis_of(const sc_cache_append& a, int j) {
   return x < a.num_axes ? x : -1;
 }
 
-// A few positions: a thread has a pair (or a dim that does not turn) of one head and position.
+// A few positions: a thread has a pair (or a dim that does not turn) of one head and position.  Its sine and cosine are
+// made again for every head, which is nothing beside the launch (64 positions of 32 + 2 x 8 heads: 5.9 us, 4.4 of them
+// a launch after another).
 template <class T, class K>
 __global__ __launch_bounds__(256) void append_few(const sc_cache_append a, int64_t total) {
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;

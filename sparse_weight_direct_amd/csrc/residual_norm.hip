@@ -1,6 +1,10 @@
 // The norms around a block with its residual sum (sparseconv_residual_norm).
 //
 //   r = x + scale gate post(y),  out = norm(r) weight + bias,  over the channels of each position
+//
+// Bound by memory, in phases: a workgroup loads, makes statistics, stores the sum, makes statistics, stores the norm, and holds its
+// values in so many registers that no other shares its CU.  8 x 2048 channels x 2048 positions, bf16, gated: 93 us, 2.9 TB/s
+// (read and written once, by the counters; a copy: 5.1).  64 single positions of 4096 channels: 6.2 us.
 #include <hip/hip_runtime.h>
 
 #include "attention.h"
@@ -28,7 +32,7 @@ __device__ __forceinline__ float over_rows(float v, float (*part)[16]) {
 //
 // A thread has PASS channels of V consecutive positions; LP lanes side by side along the positions, THREADS / LP rows of channels. The block's
 // output stays in registers from its statistics to the sum, the sum (in fp32) from its statistics to the norm.
-// Bound by memory.
+// (The channels' weights and gates in LDS beside the first loads gained nothing, and cost registers.)
 
 // Sums over the workgroup's rows of channels, for each of a lane's positions.  (part: LDS, THREADS / 64 x LP x V.)
 template <int V, int THREADS>
@@ -265,7 +269,8 @@ __global__ __launch_bounds__(THREADS) void norm_token(const sc_residual_norm a) 
   }
 }
 
-// Any sizes: 16 positions a workgroup, what it needs again it reads again.
+// Any sizes (more channels than registers hold, single positions with channels apart): 16 positions a workgroup, what it
+// needs again it reads again.
 template <class T>
 __global__ __launch_bounds__(256) void norm_any(const sc_residual_norm a, int tiles) {
   __shared__ float part[16][16];
