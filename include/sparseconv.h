@@ -556,7 +556,7 @@ typedef struct {
   int64_t q_batch, q_channel, out_batch, out_channel; /* strides */
   int64_t k_page, v_page;                             /* between pages */
   int64_t table_batch;
-  float scale, cap;                                   /* cap 0: none */
+  float scale, cap;                                   /* cap 0: none; scale, cap and scale / cap finite, and half as large again */
   int32_t dtype, B, H, G, D, L, P, width, pages;      /* G divides H */
   int32_t window;                                     /* 0: none */
   uint32_t flags;                                     /* 0 or SC_ATT_OUT_F32 */
@@ -655,7 +655,7 @@ typedef struct {
  *     r = x + scale * gate * post(y),  sum = r,  out = norm(r) * weight + bias,
  *     norm(v) = (v - m) / sqrt(mean((v - m)^2) + eps),  m = mean(v) with SC_NORM_CENTER, else 0,
  *     post(v) = norm(v) * post_weight + post_bias where there is a post_weight, else v.
- * r is normed before it is rounded.  "x itself": the same pointer and strides.  B, L >= 0, C >= 1.
+ * r is normed before it is rounded.  A mean square beyond fp32's range is infinite.  "x itself": the same pointer and strides.  B, L >= 0, C >= 1.
  * Limits: C < 2^20, L < 2^30, B*ceil(L/4) < 2^22.
  */
 sc_status sparseconv_residual_norm(const sc_residual_norm* a, void* hip_stream);

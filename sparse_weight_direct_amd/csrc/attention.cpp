@@ -70,7 +70,9 @@ sc_status sparseconv_paged_attention(const sc_paged_attention* a, void* hip_stre
     if (a->B == 0 || a->L == 0) return SC_OK;
     const int64_t es = size_of(a->dtype), os = a->flags & SC_ATT_OUT_F32 ? 4 : es, per = (int64_t)a->G * a->P * a->D;
     if (!a->q || !a->out || !a->past) return fail(SC_EINVAL, "q, out or past is NULL");
-    if (!std::isfinite(a->scale) || !std::isfinite(a->cap) || a->cap < 0) return fail(SC_EINVAL, "scale or cap is not finite, or cap < 0");
+    // (the kernels use scale log2(e), scale / cap and cap log2(e))
+    if (!std::isfinite(1.5f * a->scale) || !std::isfinite(1.5f * a->cap) || a->cap < 0 || (a->cap > 0 && !std::isfinite(a->scale / a->cap)))
+      return fail(SC_EINVAL, "scale, cap or scale / cap is not finite, or cap < 0");
     if (misaligned(a->q, es) || misaligned(a->out, os) || misaligned(a->past, 4) || misaligned(a->lengths, 4) ||
         misaligned(a->prefix, 4) || misaligned(a->slopes, 4))
       return fail(SC_EINVAL, "a pointer is not aligned to its type");

@@ -80,6 +80,11 @@ def test_attention_refusals(kw, status):
     assert _status(sc.sparseconv_paged_attention, _attend(**kw)) == status
 
 
+@pytest.mark.parametrize("kw", [dict(scale=3e38), dict(scale=-3e38), dict(cap=3e38), dict(scale=1.0, cap=1e-39), dict(scale=1e30, cap=1e-10)])
+def test_scales_that_leave_the_range_are_refused(kw):
+    assert _status(sc.sparseconv_paged_attention, _attend(**kw)) == EINVAL
+
+
 def test_attention_workspace_is_asked_for():
     far = dict(L=1, B=1, width=1000, table_batch=1000, q_channel=1, q_batch=64, out_channel=1, out_batch=64)
     need = sc.sparseconv_paged_attention_workspace(_attend(**far))
