@@ -219,14 +219,18 @@ struct Rows {
           for (int i = 0; i < 4; i++) v[i] = hidden(part, k0 + (u / 2) * kBlock, miss >> (u & ~1), u & 1, t, i) ? -kInf : v[i];
           s[u][t] = v;
         }
-    // the maximum moves where a score passes it by 2^8 (the first ones do)
+    // the maximum moves where a score passes it by 2^8 (the first ones do).  (maximum() lets a NaN through, which spoils the row
+    // as it would anyway, and takes three operands; fmaxf of matrix results is two instructions more.)
     bool moves = false;
     float most[NT];
 #pragma unroll
     for (int t = 0; t < NT; t++) {
       most[t] = -kInf;
 #pragma unroll
-      for (int u = 0; u < 2 * NB; u++) most[t] = fmaxf(most[t], fmaxf(fmaxf(s[u][t][0], s[u][t][1]), fmaxf(s[u][t][2], s[u][t][3])));
+      for (int u = 0; u < 2 * NB; u++)
+#pragma unroll
+        for (int i = 0; i < 4; i += 2)
+          most[t] = __builtin_elementwise_maximum(most[t], __builtin_elementwise_maximum(s[u][t][i], s[u][t][i + 1]));
       most[t] *= scale;
       moves |= most[t] > top[t] + 8.0f;
     }
@@ -666,9 +670,6 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
     for (int e = threadIdx.x; e < 2 * S::kBytes / 16; e += 256) reinterpret_cast<W4*>(lds)[e] = W4{0, 0, 0, 0};
     __syncthreads();
   }
-  // the rows' own part of the tiles' keys
-  const int until = r.any ? max(min(r.past + r.last + 1, r.end), r.prefix) : 0;
-  const int from = r.any && a.window ? r.past + r.first - a.window + 1 : 0;
   R rows(a, r, b, g, row0, cut.pitch, lane);
   auto walk = [&](auto odd) __attribute__((always_inline)) {
     int n = split * per, miss = 0, k0 = tiles.at(n) * KT, buffer = 0;
@@ -693,7 +694,8 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
         }
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
       }
-      if (here >= until || (here + KT <= from && here >= r.prefix)) continue;
+      // (A wavefront whose rows see nothing of the tile makes it all the same: with a way past it the compiler copied the sums of
+      // every tile to other registers, 310 instead of 290 us for 2 x 4096 positions.)
       F4 s[2 * NB][NT];
 #pragma unroll
       for (int u = 0; u < 2 * NB; u++) {
