@@ -23,8 +23,8 @@ struct AttendPlan {
   int64_t groups() const { return tiles * splits; }
 };
 
-// Tiles of rows whose queries and sums leave a wavefront's registers room for a block's keys and values.
-constexpr int attend_most_tiles(int64_t size, int dims) { return dims <= 64 ? 4 : size * dims <= 512 ? 2 : 1; }
+// Tiles of rows of a wavefront: as many as leave its registers room for a block's keys and values, and as there is use for.
+constexpr int attend_most_tiles(int64_t size, int dims) { return dims > 128 ? 1 : size == 4 && dims <= 64 ? 4 : 2; }
 constexpr int attend_staged_tiles(int64_t size, int dims) { return size * dims <= 512 ? 2 : 1; }
 
 // How the context is cut.  Single positions, 8 heads of keys of 128 dims with 4 of queries each, bf16, us:
@@ -38,8 +38,8 @@ constexpr int attend_staged_tiles(int64_t size, int dims) { return size * dims <
 //   64 of 0 to 8191             267    248   232     227    237
 //   64 of 8191 each             357    366   370     372    390
 //   fp32, 24 x 16 heads of 64 dims, 0 to 3000: 98.2, 81.9, -, 74.9, 75.4; with a window of 1024: 47.3, 43.8, -, 46.4, 53.0
-//   512 positions after 30000 (rows shared by wavefronts): 740, 388, -, 298, 312
-//   333 positions, fp16, 5 x 6 heads of 80 dims (likewise): 74.5, 49.5, -, 39.9, 46.8, with six 37.1
+//   512 positions after 30000 (keys shared by wavefronts): 715, 377, -, 271, 286
+//   333 positions, fp16, 5 x 6 heads of 80 dims (likewise): 69.9, 47.6, -, 38.9, 45.3, with six 39.5
 //
 // so enough pieces for two workgroups a CU, of six blocks of 32 keys at least, at most 32; and where there are enough without
 // cutting, four of 64 blocks at least: sequences' lengths differ as a rule, and evenly long ones lose less than that gains.
@@ -48,19 +48,19 @@ constexpr int attend_staged_tiles(int64_t size, int dims) { return size * dims <
 // From how many rows on the wavefronts share the keys, us, shared / each its own (16 heads over 4, contexts 1 x 30000,
 // 8 x 4000, 64 x 500):
 //
-//   rows        32                            48                             64                             96
-//   bf16, 64    30/21    26/18    25/17       31/25    25/24    25/23        31/27    25/25    27/24        31/27    26/27    28/22
-//   bf16, 128   41/30    35/27    38/26       41/49    35/62    39/62        41/50    37/66    41/67        42/54    38/74    43/71
-//   bf16, 256   130/99   118/102  121/99      130/112  118/138  124/125      132/113  121/140  130/143      135/185  124/214  134/202
-//   fp32, 64    82/33    59/30    53/26       82/53    59/54    54/46        82/54    60/55    60/51        83/56    61/65    60/68
-//   fp32, 128   155/58   110/62   106/54      155/62   111/75   109/64       156/63   112/76   113/75       157/107  115/128  117/109
+//   rows        16                   32                   48                   64                   96
+//   bf16, 64    29/19 23/15 24/15    29/21 23/18 25/18    29/39 24/31 25/30    29/40 24/31 27/32    30/41 25/39 28/35
+//   bf16, 128   38/28 31/22 35/22    39/39 32/30 37/31    39/42 33/42 37/30    39/41 34/41 38/33    40/52 36/52 40/62
+//   bf16, 256   74/47 69/45 79/46    75/89 72/91 82/93    75/100 72/127 84/119 76/102 74/130 88/132 78/163 78/166 92/192
+//   fp32, 64    79/26 52/21 54/21    78/33 53/28 54/27    78/53 53/46 54/46    78/53 54/49 58/51    78/56 53/65 59/68
+//   fp32, 128   146/43 99/40 103/41  147/58 101/53 103/55 148/62 99/75 104/66  147/63 102/76 110/77 149/106 104/107 115/112
 //
-// so above 32 rows for 16-bit types of more than 64 dims, else from 96 on.
+// so above 32 rows for 16-bit types (above 16 for more than 128 dims), else from 96 on.
 inline AttendPlan attend_plan(const sc_paged_attention& a, int cus) {
   AttendPlan p;
   const int64_t share = a.H / a.G, rows = share * a.L, size = a.dtype == SC_F32 ? 4 : 2;
   const int dims = a.D <= 64 ? 64 : a.D <= 128 ? 128 : 256;
-  p.staged = size == 2 && dims > 64 ? rows > 32 : rows >= 96;
+  p.staged = size == 4 ? rows >= 96 : rows > (dims > 128 ? 16 : 32);
   p.nt = p.staged ? attend_staged_tiles(size, dims) : std::min(attend_most_tiles(size, dims), rows <= 16 ? 1 : rows <= 32 ? 2 : 4);
   const int tile = p.rows();
   p.pitch = a.L < tile ? a.L : (int)(ceil_div(a.L, tile) * tile);

@@ -310,3 +310,12 @@ def test_empty_pools_are_refused():
         sc.paged_attention(t["q"], t["k_pages"][:0], t["v_pages"][:0], t["table"], t["past"])
     with pytest.raises(sc.SparseConvError):
         sc.cache_append(t["k"], t["v"], t["k_pages"][:0], t["v_pages"][:0], t["table"], t["past"])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows", [16, 17, 32, 33, 95, 96])
+def test_rows_where_the_kernel_changes(dtype, D, rows):
+    g = _gen(D + rows)
+    _check(g, dtype, 2, rows, 1, D, 1, 32, [700, 0])
+    _check(g, dtype, 2, 1, 1, D, rows, 64, [40, 333], lengths=[rows, rows - 9], window=50, prefix=[70, 0])
