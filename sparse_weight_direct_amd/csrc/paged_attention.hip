@@ -11,9 +11,9 @@
 //
 // Two kernels, for few rows (bound by the cache's bytes) and for many (bound by matrix and vector issue together), and one
 // that joins pieces of the context.  Measured, with 32 heads over 8 of 128 dims, bf16: 64 single positions after 0 to 8191
-// others 226 us, 4.8 TB/s of keys and values (where all have 8191: 357 us uncut, 6.0 TB/s); 2 x 4096 positions 317 us, 868
-// TFLOP/s (a product of 8192^3 in the library: 1185), the matrix cores busy 40% of the time, the vector units 51%;
-// 512 after 30000: 294 us.
+// others 226 us, 4.8 TB/s of keys and values (where all have 8191: 357 us uncut, 6.0 TB/s); 2 x 4096 positions 303 us, 906
+// TFLOP/s (a product of 8192^3 in the library: 1185), the matrix cores busy 46% of the time, the vector units 50%;
+// 512 after 30000: 272 us.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
