@@ -548,7 +548,9 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : NT
 
 // 16 bytes a lane, from its address or from a base that the lanes share and a byte offset of its own, to LDS byte address
 // `to` + 16 * lane (to: the same in all lanes).  Written as asm so that the compiler does not wait for it
-// before every LDS read; the wait is at the tile's end.
+// before every LDS read; the wait is at the tile's end.  The compiler keeps no wait states of what is in here either: one between m0's
+// write and the load, and five between a vector instruction that wrote a part of the base (readfirstlane, or a reload of it) and
+// the load that reads it, wherever the compiler puts that instruction.
 __device__ __forceinline__ void to_lds(uint32_t to, const void* from) {
   asm volatile(
       "s_mov_b32 m0, %0\n\t"
@@ -564,7 +566,7 @@ __device__ __forceinline__ void to_lds(uint32_t to, const void* base, uint32_t o
                           (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at);
   asm volatile(
       "s_mov_b32 m0, %0\n\t"
-      "s_nop 0\n\t"
+      "s_nop 4\n\t"
       "global_load_lds_dwordx4 %1, %2"
       :
       : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(offset), "s"(shared)
