@@ -71,8 +71,9 @@ class PagePool:
 
     def extend(self, sequences, lengths, *, width: int | None = None):
         """Room for lengths[i] more positions of sequences[i]; returns (table, past), int32 on the pool's device, for the calls
-        that write them.  The sequences' lengths grow at once.  MemoryError, and nothing changed, where there are too few
-        pages.  width: of the table (default: as few pages as hold the longest)."""
+        that write them.  The sequences' lengths grow at once: if a call that was to write them is refused, truncate() takes the
+        positions back, or the next call attends to what was never written.  MemoryError, and nothing changed, where there are too
+        few pages.  width: of the table (default: as few pages as hold the longest)."""
         sequences, lengths = list(sequences), [int(n) for n in lengths]
         if len(sequences) != len(lengths) or len(set(sequences)) != len(sequences):
             raise ValueError("a length for each sequence, and each sequence once")
@@ -107,6 +108,18 @@ class PagePool:
             self._length[s] = old + n
         self._copy(copies)
         return self.table(sequences, width=width), self._ints(past)
+
+    def truncate(self, sequence: int, length: int) -> None:
+        """Takes back the sequence's positions from `length` on, and gives back the pages that only they used."""
+        pages, P = self._pages[sequence], self.page_size
+        keep = -(-length // P)
+        if not 0 <= length <= self._length[sequence] or (length % P and pages[keep - 1] < 0):
+            raise ValueError(f"a length of {length} where the sequence has {self._length[sequence]}, or inside a page that forget() gave back")
+        for p in pages[keep:]:
+            if p >= 0:
+                self._drop(p)
+        del pages[keep:]
+        self._length[sequence] = length
 
     def _take(self) -> int:
         p = self._free.pop()
