@@ -575,7 +575,7 @@ typedef struct {
  * is a choice: an output is off by up to half a unit of dtype of its terms' magnitudes beside its own rounding; with
  * fewer rows they keep twice the bits.  Their sum is that of the rounded weights.
  * B, L >= 0.  Limits: L < 2^30, H, G <= 2^16, and fewer than 2^24 workgroups: B*G*ceil(H/G*L/16) < 2^24
- * with L rounded up to a multiple of 128 from there on.
+ * with L rounded up to a multiple of 128 from there on (fp32 of more than 128 dims with H/G*L < 96: of 16, from there on).
  */
 sc_status sparseconv_paged_attention(const sc_paged_attention* a, void* hip_stream);
 

@@ -82,10 +82,12 @@ inline int64_t attend_workspace(const sc_paged_attention& a, int cus) {
   return p.splits == 1 ? 0 : attend_rows(a, p) * p.splits * (a.D + 2) * 4;
 }
 
-// The documented limit, whatever the launch takes; the launch makes no more workgroups than that.
+// The documented limit, whatever the launch takes, and what the launch takes where that is more (tiles of 16 rows whose heads lie apart:
+// fp32 of more than 128 dims).  The factors are looked at one by one: together they pass 64 bits.
 inline bool attend_fits(const sc_paged_attention& a) {
-  const int64_t L = a.L < 128 ? a.L : ceil_div(a.L, 128) * 128;
-  return (int64_t)a.B * a.G * ceil_div((int64_t)(a.H / a.G) * L, 16) < kMostGroups;
+  if (a.B == 0 || a.L == 0) return true;
+  const int64_t L = a.L < 128 ? a.L : ceil_div(a.L, 128) * 128, heads = (int64_t)a.B * a.G, most = ceil_div((int64_t)(a.H / a.G) * L, 16);
+  return heads < kMostGroups && most < kMostGroups && heads * most < kMostGroups && heads * attend_plan(a, 256).tiles < kMostGroups;
 }
 
 // ---- Append
