@@ -69,11 +69,14 @@ __device__ __forceinline__ float column_sum(float v) {
   return v + __shfl_xor(v, 32);
 }
 
-// tanh.  16-bit types: 1 - 2 / (1 + e^2x), off by 2^-23 of 1, far inside what their weights are rounded to.
+// tanh.  16-bit types: 1 - 2 / (1 + e^2x), off by 2^-22 of 1, far inside what their weights are rounded to while the cap is small;
+// with a large one (scores are the cap times this) what counts is the error relative to the tanh, so below 1/8 its series to
+// x^5 (the next term is 2^-22 of it): off by 2^-19 of the result everywhere.
 template <class T>
 __device__ __forceinline__ float tanh_of(float x) {
   if constexpr (sizeof(T) == 4) return tanhf(x);
-  return 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + exp2_fast(2.0f * kLog2e * x));
+  const float far = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + exp2_fast(2.0f * kLog2e * x)), z = x * x;
+  return z < 0.015625f ? fmaf(x * z, fmaf(z, 2.0f / 15.0f, -1.0f / 3.0f), x) : far;
 }
 
 // Words of one or two values.
