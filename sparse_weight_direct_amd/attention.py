@@ -69,7 +69,7 @@ def paged_attention(q, k_pages, v_pages, table, past, *, lengths=None, scale=Non
     distance (slopes (H,) float32).  Visible are the positions before the sequence's end that lie in its
     prefix (prefix (B,) int32), and those up to the query's own, with a window the last `window` of
     them; where nothing is visible out is 0.  lengths (B,) int32: positions past a sequence's length give 0.
-    out may be float32 for 16-bit q.  workspace: a contiguous tensor, allocated where none is given."""
+    out may be float32 for 16-bit q, which keeps the weights in twice the bits.  workspace: a contiguous tensor, allocated where none is given."""
     return _run(_binding.paged_attention, "sparseconv_paged_attention", stream, q, k_pages, v_pages, table, past, lengths, prefix,
                 slopes, scale, cap, window, out, workspace, 3)
 

@@ -590,8 +590,8 @@ struct Stage {
   static __device__ __forceinline__ int value_piece(int d, int c) { return c ^ (CV >= 16 ? d & 15 : CV == 8 ? d >> 1 & 7 : d >> 2 & 3); }
 };
 
-// EXACT: D is DT.
-template <class T, int DT, int NT, bool EXACT>
+// EXACT: D is DT.  FINE: weights of 16-bit types are two operands, as in the kernel above.
+template <class T, int DT, int NT, bool EXACT, bool FINE>
 __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2) void attend_staged(const sc_paged_attention a, const Cut cut) {
   typedef Rows<T, DT, NT> R;
   typedef Stage<T, DT> S;
@@ -727,12 +727,12 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
       for (int d = 0; d < kEarly; d++) early[d] = value(d, 0);
       __builtin_amdgcn_s_setprio(0);
       const bool whole = rows.whole(here, gone, KT);
-      V p[NT][NB * VF], none[NT][1];
-      rows.template weigh<NB, false>(s, p, none, here, gone, whole);
+      V p[NT][NB * VF], rest[NT][FINE ? NB * VF : 1];
+      rows.template weigh<NB, FINE>(s, p, rest, here, gone, whole);
       if (odd && !whole) {
 #pragma unroll
         for (int kb = 0; kb < NB; kb++)
-          rows.template add_odd<false>(p, none, kb * VF, here + kb * kBlock, gone >> (2 * kb), [&](int d, int f) { return value(d, kb * VF + f); });
+          rows.template add_odd<FINE>(p, rest, kb * VF, here + kb * kBlock, gone >> (2 * kb), [&](int d, int f) { return value(d, kb * VF + f); });
       } else {
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
@@ -741,7 +741,10 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
           for (int d = 0; d < DM; d++) {
             const V v = f == 0 && d < kEarly ? early[d & (kEarly - 1)] : value(d, f);
 #pragma unroll
-            for (int t = 0; t < NT; t++) rows.o[d][t] = mma(v, p[t][f], rows.o[d][t]);
+            for (int t = 0; t < NT; t++) {
+              rows.o[d][t] = mma(v, p[t][f], rows.o[d][t]);
+              if constexpr (FINE) rows.o[d][t] = mma(v, rest[t][f], rows.o[d][t]);
+            }
           }
       }
     }
@@ -843,10 +846,14 @@ int launch_direct(const sc_paged_attention& a, const AttendPlan& p, const Cut& c
 template <class T, int DT, int NT>
 int launch_staged(const sc_paged_attention& a, const AttendPlan& p, const Cut& cut, hipStream_t st) {
   const int64_t blocks = (int64_t)a.B * a.G * p.groups();
+  const bool fine = sizeof(T) == 2 && (a.flags & SC_ATT_OUT_F32);
+  auto start = [&](auto exact, auto twice) {
+    hipLaunchKernelGGL((attend_staged<T, DT, NT, decltype(exact)::value, decltype(twice)::value && sizeof(T) == 2>), dim3((unsigned)blocks), dim3(256), 0, st, a, cut);
+  };
   if (a.D == DT)
-    hipLaunchKernelGGL((attend_staged<T, DT, NT, true>), dim3((unsigned)blocks), dim3(256), 0, st, a, cut);
+    fine ? start(std::true_type(), std::true_type()) : start(std::true_type(), std::false_type());
   else
-    hipLaunchKernelGGL((attend_staged<T, DT, NT, false>), dim3((unsigned)blocks), dim3(256), 0, st, a, cut);
+    fine ? start(std::false_type(), std::true_type()) : start(std::false_type(), std::false_type());
   return (int)hipGetLastError();
 }
 
