@@ -571,9 +571,11 @@ typedef struct {
  * those with t <= past + i and, with a window, past + i - t < window.  (So a prefix is seen whole by
  * every position, also from within it and from beyond the window.)  Where nothing is visible out is 0.
  * What is not visible may hold anything, infinities and NaN included.  Sums and softmax in fp32.  With 16-bit types the weights p
- * are rounded for the second product: to twice dtype's bits where out is fp32, or where a head of keys has few rows (H/G * L <= 32; more
- * than 128 dims: <= 16), and to dtype where out is of dtype and there are more, which is a choice: an output is then off by up to half a
- * unit of dtype of its terms' magnitudes beside its own rounding.  Their sum is that of the rounded weights.
+ * are rounded for the second product: to twice dtype's bits where out is fp32, where the cap is above 1024, or where a head of keys has
+ * few rows (H/G * L <= 32; more than 128 dims: <= 16), and to dtype elsewhere, which is a choice: an output is then off by up to half a
+ * unit of dtype of its terms' magnitudes beside its own rounding.  Their sum is that of the rounded weights.  tanh is off by 2^-22 of 1
+ * with 16-bit types (under caps above 1024 by 2^-19 of itself).  Sums are unnormalised with weights up to 2^8 (fp16: 2^14): values whose sums so weighted pass fp32's
+ * range give infinities or NaN.
  * B, L >= 0.  Limits: L < 2^30, H, G <= 2^16, and fewer than 2^24 workgroups: B*G*ceil(H/G*L/16) < 2^24
  * with L rounded up to a multiple of 128 from there on (fp32 of more than 128 dims with H/G*L < 96: of 16, from there on).
  */

@@ -69,13 +69,18 @@ __device__ __forceinline__ float column_sum(float v) {
   return v + __shfl_xor(v, 32);
 }
 
-// tanh.  16-bit types: 1 - 2 / (1 + e^2x), off by 2^-22 of 1, far inside what their weights are rounded to while the cap is small;
-// with a large one (scores are the cap times this) what counts is the error relative to the tanh, so below 1/8 its series to
-// x^5 (the next term is 2^-22 of it): off by 2^-19 of the result everywhere.
-template <class T>
+// tanh.  16-bit types: 1 - 2 / (1 + e^2x), off by 2^-22 of 1, which under caps up to kCap is at most 2^-12 of a weight, half a unit of fp16.  Under
+// a larger one (LARGE; scores are the cap times this) what counts is the error relative to the tanh, so below 1/8 its series to
+// x^5 (the next term is 2^-22 of it): off by 2^-19 of the result everywhere.  Those have kernels of their own: in everybody's it cost 5 x 333
+// positions of 80 dims under a cap 2 us of 39, as a branch there twice the time of every prompt (other registers spilled).
+constexpr float kCap = 1024.0f;
+
+template <class T, bool LARGE>
 __device__ __forceinline__ float tanh_of(float x) {
   if constexpr (sizeof(T) == 4) return tanhf(x);
-  const float far = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + exp2_fast(2.0f * kLog2e * x)), z = x * x;
+  const float far = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + exp2_fast(2.0f * kLog2e * x));
+  if constexpr (!LARGE) return far;
+  const float z = x * x;
   return z < 0.015625f ? fmaf(x * z, fmaf(z, 2.0f / 15.0f, -1.0f / 3.0f), x) : far;
 }
 
@@ -191,7 +196,7 @@ struct Rows {
 
   // From the products q . k of NB blocks of keys from k0 on to the weights, rounded; sums and totals follow the maximum.
   // (`miss`: two bits a block.)  With FINE, 16-bit types get what the rounding lost as a second operand.
-  template <int NB, bool FINE>
+  template <int NB, bool FINE, bool LARGE>
   __device__ __forceinline__ void weigh(F4 (&s)[2 * NB][NT], V (&p)[NT][NB * VF], V (&rest)[NT][FINE ? NB * VF : 1], int k0, int miss, bool all) {
     float scale = a.scale * kLog2e;
     if (a.cap > 0.0f || a.slopes || !(scale > 0.0f)) {  // else the maximum is looked for among the products themselves
@@ -204,7 +209,7 @@ struct Rows {
 #pragma unroll
           for (int i = 0; i < 4; i++) {
             v[i] *= by;
-            if (a.cap > 0.0f) v[i] = cap * tanh_of<T>(v[i]);
+            if (a.cap > 0.0f) v[i] = cap * tanh_of<T, LARGE>(v[i]);
             if (a.slopes) v[i] -= slope[t] * fabsf((float)(pos[t] - k0 - (u / 2) * kBlock - key_of(part, u & 1, i)));
           }
           s[u][t] = v;
@@ -369,7 +374,7 @@ __device__ __forceinline__ int page_of(const sc_paged_attention& a, const int32_
 // blocks in turn, operands straight from the cache to registers (each byte is read once), the next block's on their
 // way while one is computed, and their sums are joined at the end.  Bound by the cache's bytes, so the matrix cores have time for
 // weights of twice 16 bits: a weight and what its rounding lost are two operands, and an output is as exact as its own rounding.
-template <class T, int DT, int NT>
+template <class T, int DT, int NT, bool LARGE>
 __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : NT > 1 || (DT == 128 && sizeof(T) == 2) ? 2 : 3) void attend_direct(const sc_paged_attention a, const Cut cut) {
   typedef Rows<T, DT, NT> R;
   typedef typename R::V V;
@@ -458,7 +463,7 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : NT
       if (!kAhead) load_v(at);
       const bool whole = rows.whole(k0, miss);
       V p[NT][VF], rest[NT][R::kWide ? 1 : VF];
-      rows.template weigh<1, !R::kWide>(s, p, rest, k0, miss, whole);
+      rows.template weigh<1, !R::kWide, LARGE>(s, p, rest, k0, miss, whole);
       if (!whole) {  // nothing that is not there reaches the product
 #pragma unroll
         for (int f = 0; f < VF; f++) {
@@ -590,8 +595,9 @@ struct Stage {
   static __device__ __forceinline__ int value_piece(int d, int c) { return c ^ (CV >= 16 ? d & 15 : CV == 8 ? d >> 1 & 7 : d >> 2 & 3); }
 };
 
-// EXACT: D is DT.  FINE: weights of 16-bit types are two operands, as in the kernel above.
-template <class T, int DT, int NT, bool EXACT, bool FINE>
+// EXACT: D is DT.  FINE: weights of 16-bit types are two operands, as in the kernel above: taken for fp32 outputs, whose caller asked for more than 16
+// bits (2 x 4096 positions, bf16: 396 us, to bf16 292).  LARGE: the cap may be large.
+template <class T, int DT, int NT, bool EXACT, bool FINE, bool LARGE>
 __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2) void attend_staged(const sc_paged_attention a, const Cut cut) {
   typedef Rows<T, DT, NT> R;
   typedef Stage<T, DT> S;
@@ -728,7 +734,7 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : 2)
       __builtin_amdgcn_s_setprio(0);
       const bool whole = rows.whole(here, gone, KT);
       V p[NT][NB * VF], rest[NT][FINE ? NB * VF : 1];
-      rows.template weigh<NB, FINE>(s, p, rest, here, gone, whole);
+      rows.template weigh<NB, FINE, LARGE>(s, p, rest, here, gone, whole);
       if (odd && !whole) {
 #pragma unroll
         for (int kb = 0; kb < NB; kb++)
@@ -836,24 +842,36 @@ __global__ __launch_bounds__(256) void attend_join(const sc_paged_attention a, c
   }
 }
 
+// Caps above kCap.
+template <class T>
+bool large_cap(const sc_paged_attention& a) { return sizeof(T) == 2 && a.cap > kCap; }
+
 template <class T, int DT, int NT>
 int launch_direct(const sc_paged_attention& a, const AttendPlan& p, const Cut& cut, hipStream_t st) {
-  const int64_t blocks = (int64_t)a.B * a.G * p.groups();
-  hipLaunchKernelGGL((attend_direct<T, DT, NT>), dim3((unsigned)blocks), dim3(256), 0, st, a, cut);
+  const dim3 grid((unsigned)((int64_t)a.B * a.G * p.groups()));
+  if (large_cap<T>(a))
+    hipLaunchKernelGGL((attend_direct<T, DT, NT, sizeof(T) == 2>), grid, dim3(256), 0, st, a, cut);
+  else
+    hipLaunchKernelGGL((attend_direct<T, DT, NT, false>), grid, dim3(256), 0, st, a, cut);
   return (int)hipGetLastError();
 }
 
+// 16-bit types have forms with twice the weights' bits for fp32 outputs; under a large cap there is one for all.
 template <class T, int DT, int NT>
 int launch_staged(const sc_paged_attention& a, const AttendPlan& p, const Cut& cut, hipStream_t st) {
-  const int64_t blocks = (int64_t)a.B * a.G * p.groups();
-  const bool fine = sizeof(T) == 2 && (a.flags & SC_ATT_OUT_F32);
-  auto start = [&](auto exact, auto twice) {
-    hipLaunchKernelGGL((attend_staged<T, DT, NT, decltype(exact)::value, decltype(twice)::value && sizeof(T) == 2>), dim3((unsigned)blocks), dim3(256), 0, st, a, cut);
-  };
-  if (a.D == DT)
-    fine ? start(std::true_type(), std::true_type()) : start(std::true_type(), std::false_type());
+  constexpr bool k16 = sizeof(T) == 2;
+  const dim3 grid((unsigned)((int64_t)a.B * a.G * p.groups()));
+  const bool fine = k16 && (a.flags & SC_ATT_OUT_F32);
+  if (large_cap<T>(a))
+    hipLaunchKernelGGL((attend_staged<T, DT, NT, false, k16, k16>), grid, dim3(256), 0, st, a, cut);
+  else if (a.D == DT && fine)
+    hipLaunchKernelGGL((attend_staged<T, DT, NT, true, k16, false>), grid, dim3(256), 0, st, a, cut);
+  else if (a.D == DT)
+    hipLaunchKernelGGL((attend_staged<T, DT, NT, true, false, false>), grid, dim3(256), 0, st, a, cut);
+  else if (fine)
+    hipLaunchKernelGGL((attend_staged<T, DT, NT, false, k16, false>), grid, dim3(256), 0, st, a, cut);
   else
-    fine ? start(std::false_type(), std::true_type()) : start(std::false_type(), std::false_type());
+    hipLaunchKernelGGL((attend_staged<T, DT, NT, false, false, false>), grid, dim3(256), 0, st, a, cut);
   return (int)hipGetLastError();
 }
 
