@@ -610,7 +610,7 @@ typedef struct {
  * Turns the pairs (x_j, x_{j+pairs}) of the first 2*pairs dims of every head of q and k by
  * freqs[j] * positions[b, axes[j], i] (a pair whose axis is outside 0 .. num_axes-1 stays), and writes k and
  * v of the new positions into the cache; q goes to q_out, 0 past a sequence's length.  Angles are
- * reduced in fp64, so far positions are as exact as near ones.  Positions at or past width*P, or on no page, are not
+ * reduced in fp64, so far positions are as exact as near ones; sines and cosines are off by 2^-22.9.  Positions at or past width*P, or on no page, are not
  * written.  B, L >= 0.  Limits: L < 2^30, H, G <= 2^16, and with W = H + 2 G (2 G without q) B*W*D*L < 2^32 where L < 16, else
  * B*(ceil(L/64) + 1)*(ceil(W/8) + 1) < 2^24.
  */

@@ -4,7 +4,9 @@ One tensor holds every layer's keys and values, (2 * layers, pages, values a pag
 cache_copy moves a page in all of them.  A sequence is a list of pages and a length; sequences may share
 pages (fork), and a page that a sequence is about to write is its own: extend() copies a shared one first.
 The counting is the host's alone (nothing is read back); copies and tables are made on the current
-stream, in order with the calls that use them.
+stream, in order with the calls that use them.  Each list that goes to the GPU (extend: a table and a past, and the pages to copy where
+there are any) is copied from pageable memory, so the host waits there until the stream has come to it, and none of it can be captured
+into a graph: a graph's steps advance a past of their own, over a table that was extended before.
 """
 from __future__ import annotations
 

@@ -43,7 +43,9 @@ constexpr int attend_staged_tiles(int64_t size, int dims) { return size * dims <
 //
 // so enough pieces for two workgroups a CU, of six blocks of 32 keys at least, at most 32; and where there are enough without
 // cutting, four of 64 blocks at least: sequences' lengths differ as a rule, and evenly long ones lose less than that gains.
-// Single positions take a power of two of them (1 of 8000 in 31: 20.1).
+// Single positions take a power of two of them (1 of 8000 in 31: 20.1).  The six blocks rest on the sequences of 250 and 777; between
+// those, and for more than the two chunks of many rows above (333 positions lose 2% by it), nothing is measured.  The table's width is
+// what is counted, whatever a window leaves of it.
 //
 // From how many rows on the wavefronts share the keys, us, shared / each its own (16 heads over 4, contexts 1 x 30000,
 // 8 x 4000, 64 x 500):

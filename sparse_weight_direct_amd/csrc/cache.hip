@@ -6,7 +6,6 @@
 #include "attention.h"
 #include "attention_plan.h"
 #include "sequence_device.h"
-#include "xcd.h"
 
 namespace sc {
 

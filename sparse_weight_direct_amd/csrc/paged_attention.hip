@@ -11,9 +11,9 @@
 //
 // Two kernels, for few rows (bound by the cache's bytes) and for many (bound by matrix and vector issue together), and one
 // that joins pieces of the context.  Measured, with 32 heads over 8 of 128 dims, bf16: 64 single positions after 0 to 8191
-// others 226 us, 4.8 TB/s of keys and values (where all have 8191: 357 us uncut, 6.0 TB/s); 2 x 4096 positions 303 us, 906
-// TFLOP/s (a product of 8192^3 in the library: 1185), the matrix cores busy 46% of the time, the vector units 50%;
-// 512 after 30000: 272 us.
+// others 230 us, 4.7 TB/s of keys and values (where all have 8191: 357 us uncut, 6.0 TB/s); 2 x 4096 positions 302 us, 911
+// TFLOP/s (a product of 8192^3 in the library: 1185), the matrix cores busy 45% of the time, the vector units 50%;
+// 512 after 30000: 271 us.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -21,7 +21,6 @@
 #include "attention.h"
 #include "attention_plan.h"
 #include "matrix_device.h"
-#include "xcd.h"
 
 namespace sc {
 
@@ -552,7 +551,8 @@ __global__ __launch_bounds__(256, (2 + NT) * DT * (int)sizeof(T) > 1024 ? 1 : NT
 // A workgroup has 64 NT rows of one head of keys, 16 NT a wavefront, and walks its piece of the context in tiles of KT
 // keys, which it copies from the pages to LDS without passing registers, one tile ahead.  In LDS a row's
 // 16-byte pieces are dealt out by an exclusive or with the row, so that the sixteen rows that a read takes
-// lie in sixteen different places of 256 bytes.
+// lie in sixteen different places of 256 bytes.  NT is 2 and KT 64 up to 128 dims of 16 bits and 64 of fp32; else KT is 32, with NT 2
+// for 256 dims of 16 bits and 128 of fp32 and 1 for 256 of fp32 (attend_staged_tiles, Stage).
 
 // 16 bytes a lane, from its address or from a base that the lanes share and a byte offset of its own, to LDS byte address
 // `to` + 16 * lane (to: the same in all lanes).  Written as asm so that the compiler does not wait for it
