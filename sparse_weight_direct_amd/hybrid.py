@@ -46,6 +46,7 @@ class AttentionLayer:
                                       for n, w in weights.items()} for W in (length, 1))
         self._rotary = dict(freqs=None if freqs is None else freqs.detach(), axes=axes, interleaved=interleaved)
         self._attend = dict(scale=scale, cap=cap, window=window, slopes=None if slopes is None else slopes.detach())
+        self._fit = None  # sizes of a call that the operators take
         if self.k_pages.is_cuda:  # one idle sequence: everything is looked at, nothing of the cache is written
             table, past = (torch.full(s, -1, dtype=torch.int32, device=self.k_pages.device) for s in ((1, 1), (1,)))
             q, k = (self.k_pages.new_zeros(1, n * self.D) for n in (self.H, self.G))
@@ -62,13 +63,16 @@ class AttentionLayer:
                 raise ValueError(f"positions must be (B, axes, {L}) with contiguous positions: {tuple(positions.shape)}, strides {positions.stride()}")
             none = positions[:, :, :0]
         k = u.new_empty(B, G * D, 0)
-        cache_append(k, k, self.k_pages, self.v_pages, table, past, q=u.new_empty(B, H * D, 0), positions=none, lengths=lengths, **self._rotary)
+        cache_append(k, k, self.k_pages, self.v_pages, table, past, positions=none, lengths=lengths, **self._rotary)
         paged_attention(u.new_empty(B, H * D, 0, dtype=self.k_pages.dtype), self.k_pages, self.v_pages, table, past, lengths=lengths,
                         prefix=prefix, **self._attend)
-        paged_attention_workspace(B, H, L, self.k_pages, table.shape[1])
-        heads = H + 2 * G
-        if B * L * heads * D >= 2 ** 32 if L < 16 else B * (-(-L // 64) + 1) * (-(-heads // 8) + 1) >= 2 ** 24:
-            raise ValueError(f"{B} sequences of {L} positions are more than one cache_append takes")
+        sizes = B, L, table.shape[1]
+        if sizes != self._fit:  # (the last that did)
+            paged_attention_workspace(B, H, L, self.k_pages, table.shape[1])
+            heads = H + 2 * G
+            if B * L * heads * D >= 2 ** 32 if L < 16 else B * (-(-L // 64) + 1) * (-(-heads // 8) + 1) >= 2 ** 24:
+                raise ValueError(f"{B} sequences of {L} positions are more than one cache_append takes")
+            self._fit = sizes
 
     def _parts(self, qkv):
         q, k = self.H * self.D, (self.H + self.G) * self.D
